@@ -22,6 +22,7 @@ QLORA_F32, QLORA_BF16 = 0, 1
 QLORA_CB_NF4, QLORA_CB_INT4, QLORA_CB_FP4 = 0, 1, 2
 CODEBOOKS = {"nf4": QLORA_CB_NF4, "int4": QLORA_CB_INT4, "fp4": QLORA_CB_FP4}
 QLORA_OP_DOUBLE_QUANT, QLORA_OP_LINEAR_FWD, QLORA_OP_LINEAR_BWD = 0, 1, 2
+QLORA_OP_NORM_BWD = 3
 BLOCK, CHUNK, MAX_RANK = 64, 256, 128
 
 EXPORTED = ("qlora_quantize", "qlora_double_quant", "qlora_dequantize", "qlora_linear_fwd",
@@ -29,6 +30,7 @@ EXPORTED = ("qlora_quantize", "qlora_double_quant", "qlora_dequantize", "qlora_l
             "qlora_quantize_cb", "qlora_dequantize_cb", "qlora_dequantize_nodq", "qlora_codebook_levels",
             "qlora_linear_fwd_cb", "qlora_linear_bwd_cb", "qlora_merge_adapter_cb", "qlora_merge_requantize_cb",
             "qlora_silu_gate_fwd", "qlora_silu_gate_bwd", "qlora_grad_sum", "qlora_double_quant_noalloc",
+            "qlora_norm_fwd", "qlora_norm_bwd",
             "qlora_workspace_size", "qlora_stream_probe",
             "qlora_status_string", "qlora_nf4_levels", "qlora_set_timing_events")
 
@@ -72,6 +74,8 @@ def _load():
     L.qlora_silu_gate_fwd.argtypes = [vp, vp, i64, vp, vp]
     L.qlora_silu_gate_bwd.argtypes = [vp, vp, vp, i64, vp, vp, vp]
     L.qlora_grad_sum.argtypes = [ctypes.POINTER(vp), i32, i64, vp, vp]
+    L.qlora_norm_fwd.argtypes = [vp, st, vp, vp, vp, f32, vp, f32, i64, i64, vp, vp, vp, vp, vp]
+    L.qlora_norm_bwd.argtypes = [vp, vp, st, vp, vp, vp, vp, vp, vp, f32, vp, i64, i64, vp, vp, vp, vp, vp, vp, sz, vp]
     L.qlora_stream_probe.argtypes = [i32, i32, i32, i32, vp, vp, i64, vp]
     L.qlora_adamw_step.argtypes = [vp, vp, vp, vp, i64, i64, f32, f32, f32, f32, f32, vp, vp]
     L.qlora_workspace_size.argtypes = [st, i64, i64, i64, i32, ctypes.POINTER(sz)]
@@ -105,6 +109,26 @@ def _dev_check(*ts):
     for t in ts:
         if t is not None and (not t.is_cuda or not t.is_contiguous()):
             raise ValueError("tensors must be contiguous and on the GPU")
+
+
+def _want(name: str, t: Optional[torch.Tensor], dtype, shape, device):
+    """Refuses a tensor that the C call would misread: its type, shape, layout or device."""
+    if t is None:
+        return
+    if not t.is_cuda or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and on {device}")
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} is {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+
+
+def _call(device, name: str, *args):
+    """Entry point `name` on `device`'s current stream, with that device current."""
+    stream = _stream(device)
+    if torch.cuda.current_device() == device.index:
+        _check(getattr(lib, name)(*args, stream), name)
+    else:
+        with torch.cuda.device(device):
+            _check(getattr(lib, name)(*args, stream), name)
 
 
 def nf4_levels() -> list:
@@ -404,3 +428,91 @@ def qlora_grad_sum(parts, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     arr = (ctypes.c_void_p * len(parts))(*[p.data_ptr() for p in parts])
     _check(lib.qlora_grad_sum(arr, len(parts), n, _ptr(out), _stream(out.device)), "qlora_grad_sum")
     return out
+
+
+# ---------------------------------------------------------------------------
+# Norms before and after a block, with its gate and residual scale
+# ---------------------------------------------------------------------------
+
+_STREAM_TYPES = {torch.float32: QLORA_F32, torch.bfloat16: QLORA_BF16}
+
+
+def _stream_type(t: torch.Tensor) -> int:
+    if t.dim() != 2 or t.dtype not in _STREAM_TYPES:
+        raise ValueError("the residual stream is a [rows][width] float32 or bf16 tensor")
+    return _STREAM_TYPES[t.dtype]
+
+
+def qlora_norm_fwd(R: torch.Tensor, Y: Optional[torch.Tensor] = None, w_pre: Optional[torch.Tensor] = None,
+                   w_post: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None, alpha: float = 1.0,
+                   eps: float = 1e-6, R_out: Optional[torch.Tensor] = None, N: Optional[torch.Tensor] = None,
+                   rstd_pre: Optional[torch.Tensor] = None, rstd_post: Optional[torch.Tensor] = None):
+    """R_out = R + alpha * gate * u with u = Y or RMS norm(Y) * w_post, and
+    N = RMS norm(R_out) * w_pre -> (R_out, N, rstd_pre, rstd_post).  Without Y (the norm
+    before the first block) R_out is R; without w_pre N and rstd_pre are None."""
+    dt = _stream_type(R)
+    M, h = R.shape
+    dev = R.device
+    if Y is None:
+        R_out = R if R_out is None else R_out
+    elif R_out is None:
+        R_out = torch.empty_like(R)
+    if w_pre is not None:
+        N = torch.empty(M, h, dtype=torch.bfloat16, device=dev) if N is None else N
+        rstd_pre = torch.empty(M, dtype=torch.float32, device=dev) if rstd_pre is None else rstd_pre
+    if w_post is not None and rstd_post is None:
+        rstd_post = torch.empty(M, dtype=torch.float32, device=dev)
+    for name, t, dtype, shape in (("R", R, R.dtype, (M, h)), ("R_out", R_out, R.dtype, (M, h)),
+                                  ("Y", Y, torch.bfloat16, (M, h)), ("N", N, torch.bfloat16, (M, h)),
+                                  ("w_pre", w_pre, torch.float32, (h,)), ("w_post", w_post, torch.float32, (h,)),
+                                  ("gate", gate, torch.float32, (h,)), ("rstd_pre", rstd_pre, torch.float32, (M,)),
+                                  ("rstd_post", rstd_post, torch.float32, (M,))):
+        _want(name, t, dtype, shape, dev)
+    _call(dev, "qlora_norm_fwd", _ptr(R), dt, _ptr(Y), _ptr(w_post), _ptr(gate), float(alpha), _ptr(w_pre),
+          float(eps), M, h, _ptr(R_out), _ptr(N), _ptr(rstd_post), _ptr(rstd_pre))
+    return R_out, N, rstd_pre, rstd_post
+
+
+def qlora_norm_bwd(dN: Optional[torch.Tensor], dR_out: Optional[torch.Tensor], R_out: Optional[torch.Tensor],
+                   Y: Optional[torch.Tensor] = None, rstd_pre: Optional[torch.Tensor] = None,
+                   rstd_post: Optional[torch.Tensor] = None, w_pre: Optional[torch.Tensor] = None,
+                   w_post: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None, alpha: float = 1.0,
+                   weight_grads: bool = False, block: bool = True, dR: Optional[torch.Tensor] = None,
+                   dY: Optional[torch.Tensor] = None, dw_pre: Optional[torch.Tensor] = None,
+                   dw_post: Optional[torch.Tensor] = None, dgate: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None):
+    """Backward of qlora_norm_fwd for the gradients dN of N and dR_out of R_out ->
+    (dR, dY, dw_pre, dw_post, dgate).  `block` False: the forward had no Y (dY is None).
+    `weight_grads`: allocate the gradient of every weight given (or pass the wanted
+    buffers); the others are None."""
+    like = R_out if R_out is not None else dR_out
+    if like is None:
+        raise ValueError("qlora_norm_bwd needs R_out or dR_out")
+    dt = _stream_type(like)
+    M, h = like.shape
+    dev = like.device
+    dR = torch.empty_like(like) if dR is None else dR
+    if block and dY is None:
+        dY = torch.empty(M, h, dtype=torch.bfloat16, device=dev)
+    if weight_grads:
+        new = lambda w, d: torch.empty(h, dtype=torch.float32, device=dev) if w is not None and d is None else d
+        dw_pre, dw_post, dgate = new(w_pre, dw_pre), new(w_post, dw_post), new(gate, dgate)
+    sums = dw_pre is not None or dw_post is not None or dgate is not None
+    if sums and workspace is None:
+        workspace = torch.empty(workspace_size(QLORA_OP_NORM_BWD, M, h), dtype=torch.uint8, device=dev)
+    for name, t, dtype, shape in (("dN", dN, torch.bfloat16, (M, h)), ("dR_out", dR_out, like.dtype, (M, h)),
+                                  ("R_out", R_out, like.dtype, (M, h)), ("Y", Y, torch.bfloat16, (M, h)),
+                                  ("rstd_pre", rstd_pre, torch.float32, (M,)),
+                                  ("rstd_post", rstd_post, torch.float32, (M,)),
+                                  ("w_pre", w_pre, torch.float32, (h,)), ("w_post", w_post, torch.float32, (h,)),
+                                  ("gate", gate, torch.float32, (h,)), ("dR", dR, like.dtype, (M, h)),
+                                  ("dY", dY, torch.bfloat16, (M, h)), ("dw_pre", dw_pre, torch.float32, (h,)),
+                                  ("dw_post", dw_post, torch.float32, (h,)), ("dgate", dgate, torch.float32, (h,)),
+                                  ("workspace", workspace, torch.uint8,
+                                   () if workspace is None else (workspace.numel(),))):
+        _want(name, t, dtype, shape, dev)
+    _call(dev, "qlora_norm_bwd", _ptr(dN), _ptr(dR_out), dt, _ptr(R_out), _ptr(Y if block else None),
+          _ptr(rstd_post), _ptr(rstd_pre), _ptr(w_post), _ptr(gate), float(alpha), _ptr(w_pre), M, h, _ptr(dR),
+          _ptr(dY), _ptr(dw_pre), _ptr(dw_post), _ptr(dgate), _ptr(workspace),
+          0 if workspace is None else workspace.numel())
+    return dR, dY, dw_pre, dw_post, dgate

@@ -6,17 +6,25 @@
 #include "codec.h"
 #include "glue.h"
 #include "linear.h"
+#include "norm.h"
 #include "optim.h"
 #include "stream.h"
 
 #include <cmath>
 #include <cstddef>
+#include <initializer_list>
 
 using namespace ql;
 
 namespace {
 
 inline bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+bool aligned16(std::initializer_list<const void *> ps) {
+  for (const void *p : ps)
+    if (!aligned(p, 16)) return false;
+  return true;
+}
 
 inline qlora_status_t launch_status(hipError_t e) { return e == hipSuccess ? QLORA_OK : QLORA_ERR_LAUNCH; }
 
@@ -137,6 +145,50 @@ qlora_status_t qlora_grad_sum(const uint16_t *const *parts, int32_t k, int64_t n
   return launch_status(launch_grad_sum(sp, n, out, reinterpret_cast<hipStream_t>(stream)));
 }
 
+qlora_status_t qlora_norm_fwd(const void *R, qlora_dtype_t r_dtype, const uint16_t *Y, const float *w_post,
+                              const float *gate, float alpha, const float *w_pre, float eps, int64_t M, int64_t h,
+                              void *R_out, uint16_t *N, float *rstd_post, float *rstd_pre, void *stream) {
+  if (!R || (!Y && !w_pre) || M < 1 || h < 1) return QLORA_ERR_INVALID_VALUE;
+  if (r_dtype != QLORA_F32 && r_dtype != QLORA_BF16) return QLORA_ERR_INVALID_VALUE;
+  if (!Y && (w_post || gate || (R_out && R_out != R))) return QLORA_ERR_INVALID_VALUE;
+  if (Y && (!R_out || !std::isfinite(alpha))) return QLORA_ERR_INVALID_VALUE;
+  if (w_pre && !N) return QLORA_ERR_INVALID_VALUE;
+  if ((w_pre || w_post) && (!(eps > 0.0f) || !std::isfinite(eps))) return QLORA_ERR_INVALID_VALUE;
+  if (!aligned16({R, Y, w_post, gate, w_pre, R_out, N, rstd_post, rstd_pre})) return QLORA_ERR_INVALID_VALUE;
+  if (N && (N == R || N == Y || N == R_out)) return QLORA_ERR_INVALID_VALUE;
+  if (R_out && R_out == Y) return QLORA_ERR_INVALID_VALUE;
+  if (h > kMaxNormWidth || M > ((int64_t)1 << 40) / h) return QLORA_ERR_UNSUPPORTED;
+  const NormFwdArgs a{R, Y, w_post, gate, w_pre, alpha, eps, M, h, Y ? R_out : nullptr, N,
+                      w_post ? rstd_post : nullptr, rstd_pre};
+  return launch_status(launch_norm_fwd(a, r_dtype == QLORA_BF16, reinterpret_cast<hipStream_t>(stream)));
+}
+
+qlora_status_t qlora_norm_bwd(const uint16_t *dN, const void *dR_out, qlora_dtype_t r_dtype, const void *R_out,
+                              const uint16_t *Y, const float *rstd_post, const float *rstd_pre, const float *w_post,
+                              const float *gate, float alpha, const float *w_pre, int64_t M, int64_t h, void *dR,
+                              uint16_t *dY, float *dw_pre, float *dw_post, float *dgate, void *workspace,
+                              size_t ws_bytes, void *stream) {
+  if (!dR || M < 1 || h < 1 || (r_dtype != QLORA_F32 && r_dtype != QLORA_BF16)) return QLORA_ERR_INVALID_VALUE;
+  if (w_pre ? (!dN || !R_out || !rstd_pre) : (!dR_out || dw_pre)) return QLORA_ERR_INVALID_VALUE;
+  if (!dY && (Y || w_post || gate || dw_post || dgate)) return QLORA_ERR_INVALID_VALUE;
+  if (dY && !std::isfinite(alpha)) return QLORA_ERR_INVALID_VALUE;
+  if (w_post ? (!Y || !rstd_post) : dw_post != nullptr) return QLORA_ERR_INVALID_VALUE;
+  if (dgate && (!gate || !Y)) return QLORA_ERR_INVALID_VALUE;
+  if (!aligned16({dN, dR_out, R_out, Y, rstd_post, rstd_pre, w_post, gate, w_pre, dR, dY, dw_pre, dw_post, dgate}))
+    return QLORA_ERR_INVALID_VALUE;
+  if (dR == dN || dR == R_out || dR == Y || dR == dY) return QLORA_ERR_INVALID_VALUE;
+  if (dY && (dY == dN || dY == R_out || dY == dR_out || dY == Y)) return QLORA_ERR_INVALID_VALUE;
+  if (h > kMaxNormWidth || M > ((int64_t)1 << 40) / h) return QLORA_ERR_UNSUPPORTED;
+  if (dw_pre || dw_post || dgate) {
+    if (!workspace || !aligned(workspace, 256) || ws_bytes < round256(norm_bwd_workspace(M, h)))
+      return QLORA_ERR_INVALID_VALUE;
+  }
+  const NormBwdArgs a{w_pre ? dN : nullptr, dR_out, R_out, w_post || dgate ? Y : nullptr, rstd_post, rstd_pre, w_post,
+                      gate, w_pre, alpha, M, h, dR, dY, dw_pre, dw_post, dgate};
+  return launch_status(launch_norm_bwd(a, r_dtype == QLORA_BF16, reinterpret_cast<float *>(workspace),
+                                       reinterpret_cast<hipStream_t>(stream)));
+}
+
 qlora_status_t qlora_stream_probe(int32_t rd, int32_t wr, int32_t depth, int32_t blocks, const void *src, void *dst,
                                   int64_t n_tiles, void *stream) {
   const bool kind = (rd == 1 && wr == 0) || (rd == 4 && wr == 1) || (rd == 1 && wr == 4);
@@ -167,6 +219,10 @@ qlora_status_t qlora_workspace_size(qlora_op_t op, int64_t a, int64_t b, int64_t
       if (a < 1 || b < 64 || c < 64 || r < 0 || r > QLORA_MAX_RANK) return QLORA_ERR_INVALID_VALUE;
       *bytes = round256(op == QLORA_OP_LINEAR_FWD ? linear_fwd_workspace(a, b, c, r)
                                                   : linear_bwd_workspace(a, b, c, r));
+      return QLORA_OK;
+    case QLORA_OP_NORM_BWD:
+      if (a < 1 || b < 1 || b > kMaxNormWidth) return QLORA_ERR_INVALID_VALUE;
+      *bytes = round256(norm_bwd_workspace(a, b));
       return QLORA_OK;
   }
   return QLORA_ERR_INVALID_VALUE;

@@ -68,7 +68,8 @@ typedef enum { QLORA_CB_NF4 = 0, QLORA_CB_INT4 = 1, QLORA_CB_FP4 = 2 } qlora_cod
 typedef enum {
   QLORA_OP_DOUBLE_QUANT = 0, /* a = number of block scales */
   QLORA_OP_LINEAR_FWD = 1,   /* a = M tokens, b = h, c = o */
-  QLORA_OP_LINEAR_BWD = 2    /* a = M tokens, b = h, c = o */
+  QLORA_OP_LINEAR_BWD = 2,   /* a = M tokens, b = h, c = o */
+  QLORA_OP_NORM_BWD = 3      /* a = M rows, b = h */
 } qlora_op_t;
 
 #define QLORA_BLOCK 64      /* weights per first-level scale ([MC] "2. Double quantization") */
@@ -327,6 +328,56 @@ qlora_status_t qlora_silu_gate_fwd(const uint16_t *G, const uint16_t *U, int64_t
 qlora_status_t qlora_silu_gate_bwd(const uint16_t *G, const uint16_t *U, const uint16_t *dH, int64_t n, uint16_t *dG,
                                    uint16_t *dU, void *stream);
 qlora_status_t qlora_grad_sum(const uint16_t *const *parts, int32_t k, int64_t n, uint16_t *out, void *stream);
+
+/*
+ * Norms before and after a block, fused with the block's gate and residual scale.
+ * The pages' linears sit in the blocks of a LLaMA-like transformer ([MC] "A closer
+ * look: Design choices and memory costs"); between two blocks the residual stream R
+ * takes the block's output Y and is normalised for the next block.  With
+ * rstd(x) = 1 / sqrt(mean(x^2) + eps) over a row of h values:
+ *   u     = Y, or Y * rstd(Y) * w_post where the block has a norm after it
+ *   R_out = R + alpha * gate * u
+ *   N     = R_out * rstd(R_out) * w_pre
+ * Arithmetic is float32 and each output is rounded once; N is formed from the
+ * float32 R_out, before it is rounded to a bf16 stream.  M rows, 1 <= h <= 16384
+ * (any h; a wider row is QLORA_ERR_UNSUPPORTED).  Y, N, dN and dY are [M][h] bf16;
+ * the stream (R, R_out, dR_out, dR) is [M][h] of r_dtype; weights, gate and their
+ * gradients are [h] float32, rstd_post and rstd_pre [M] float32.  All pointers are
+ * 16-byte aligned.  Squares of magnitudes above 1e18 overflow float32: rows that
+ * hold such values give unspecified results, like non-finite ones.
+ *
+ * qlora_norm_fwd
+ *  Y       may be NULL (the norm before the first block): then w_post and gate are
+ *          NULL, R_out is R itself and its pointer may be NULL or R (not stored).
+ *  w_post  NULL: no norm after the block.   gate  NULL: 1.   alpha  finite.
+ *  w_pre   NULL: no N (the residual update alone); N and rstd_pre are not used.
+ *  R_out   may be R (in place).  rstd_post and rstd_pre may be NULL (inference);
+ *          they are what the backward takes.  At least one of Y and w_pre is given.
+ *
+ * qlora_norm_bwd   for the gradients dN of N and dR_out of R_out, with
+ *   x = R_out * rstd_pre,  d = dN * w_pre,  y = Y * rstd_post:
+ *     dR   = dR_out + rstd_pre * (d - x * mean(d * x))         (the gradient of R)
+ *     dY   = alpha * gate * dR, or with a norm after the block, du being that:
+ *            rstd_post * (du * w_post - y * mean(du * w_post * y))
+ *     dw_pre = sum dN * x    dw_post = sum du * y    dgate = sum alpha * dR * u
+ *  (dR enters the later lines in float32.)
+ *  w_pre   NULL: no N; dN, R_out, rstd_pre and dw_pre are not used and dR = dR_out.
+ *  dR_out  NULL: zero (only with w_pre).   dR may be dR_out (in place).
+ *  dY      NULL: there was no block output; Y, w_post, gate, dw_post, dgate are NULL.
+ *  Y       needed with w_post and with dgate.
+ *  dw_pre, dw_post, dgate   NULL: that weight is frozen.  The sums over rows run in
+ *          a fixed order (no atomics).
+ *  workspace: qlora_workspace_size(QLORA_OP_NORM_BWD, M, h, 0, 0) bytes, 256-byte
+ *          aligned, needed only when one of the three is wanted.
+ */
+qlora_status_t qlora_norm_fwd(const void *R, qlora_dtype_t r_dtype, const uint16_t *Y, const float *w_post,
+                              const float *gate, float alpha, const float *w_pre, float eps, int64_t M, int64_t h,
+                              void *R_out, uint16_t *N, float *rstd_post, float *rstd_pre, void *stream);
+qlora_status_t qlora_norm_bwd(const uint16_t *dN, const void *dR_out, qlora_dtype_t r_dtype, const void *R_out,
+                              const uint16_t *Y, const float *rstd_post, const float *rstd_pre, const float *w_post,
+                              const float *gate, float alpha, const float *w_pre, int64_t M, int64_t h, void *dR,
+                              uint16_t *dY, float *dw_pre, float *dw_post, float *dgate, void *workspace,
+                              size_t ws_bytes, void *stream);
 
 /* Workspace bytes an entry point needs (always a multiple of 256; may be 0). */
 qlora_status_t qlora_workspace_size(qlora_op_t op, int64_t a, int64_t b, int64_t c, int32_t r,

@@ -1,0 +1,54 @@
+"""Refusals of the training step's operators around the linears, on the CPU: every bad
+argument is turned away before anything is launched."""
+import ctypes
+
+import pytest
+
+nf4 = pytest.importorskip("bit_quantized_fine_nf4_amd")
+lib = nf4.lib
+
+OK, INV, UNS = nf4.QLORA_OK, nf4.QLORA_ERR_INVALID_VALUE, nf4.QLORA_ERR_UNSUPPORTED
+A = [ctypes.c_void_p(0x100000 + 0x10000 * i) for i in range(24)]   # distinct, aligned, never dereferenced
+ODD = ctypes.c_void_p(0x100002)
+NAN = float("nan")
+
+
+def norm_fwd(R=A[0], dt=1, Y=A[1], w_post=A[2], gate=A[3], alpha=1.0, w_pre=A[4], eps=1e-6, M=4, h=64, R_out=A[5],
+             N=A[6], rq=A[7], rp=A[8]):
+    return lib.qlora_norm_fwd(R, dt, Y, w_post, gate, alpha, w_pre, eps, M, h, R_out, N, rq, rp, None)
+
+
+def norm_bwd(dN=A[0], dR_out=A[1], dt=1, R_out=A[2], Y=A[3], rq=A[4], rp=A[5], w_post=A[6], gate=A[7], alpha=1.0,
+             w_pre=A[8], M=4, h=64, dR=A[9], dY=A[10], dwp=A[11], dwq=A[12], dg=A[13], ws=A[14], wb=1 << 30):
+    return lib.qlora_norm_bwd(dN, dR_out, dt, R_out, Y, rq, rp, w_post, gate, alpha, w_pre, M, h, dR, dY, dwp, dwq, dg,
+                              ws, wb, None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(R=None), dict(dt=2), dict(M=0), dict(h=0), dict(M=-1), dict(R=ODD), dict(Y=ODD), dict(w_pre=ODD),
+    dict(rp=ODD), dict(eps=0.0), dict(eps=NAN), dict(eps=float("inf")), dict(alpha=NAN), dict(N=None), dict(R_out=None),
+    dict(Y=None), dict(Y=None, w_post=None), dict(Y=None, w_post=None, gate=None),   # R_out is then R
+    dict(Y=None, w_post=None, gate=None, R_out=None, w_pre=None), dict(N=A[0]), dict(N=A[5]), dict(R_out=A[1]),
+])
+def test_norm_fwd_refusals(bad):
+    assert norm_fwd(**bad) == INV
+
+
+@pytest.mark.parametrize("bad", [
+    dict(dR=None), dict(dt=3), dict(M=0), dict(h=-1), dict(dN=None), dict(R_out=None), dict(rp=None), dict(dR=ODD),
+    dict(w_pre=None), dict(w_pre=None, dwp=None, dR_out=None), dict(dY=None), dict(Y=None), dict(rq=None),
+    dict(w_post=None), dict(gate=None), dict(alpha=NAN), dict(ws=None), dict(wb=16), dict(ws=ctypes.c_void_p(0x100010)),
+    dict(dR=A[0]), dict(dR=A[2]), dict(dR=A[10]), dict(dY=A[0]), dict(dY=A[1]), dict(dY=A[3]),
+    dict(w_post=None, dwq=None, Y=None),      # the gate's gradient needs Y
+])
+def test_norm_bwd_refusals(bad):
+    assert norm_bwd(**bad) == INV
+
+
+def test_norm_limits():
+    assert norm_fwd(h=16385) == UNS and norm_bwd(h=16385) == UNS
+    assert norm_fwd(M=1 << 40, h=64) == UNS and norm_bwd(M=1 << 40, h=64) == UNS
+    assert nf4.workspace_size(nf4.QLORA_OP_NORM_BWD, 5, 100) % 256 == 0
+    for a, b in ((0, 64), (4, 0), (4, 16385)):
+        with pytest.raises(nf4.QloraError):
+            nf4.workspace_size(nf4.QLORA_OP_NORM_BWD, a, b)
