@@ -22,7 +22,7 @@ QLORA_F32, QLORA_BF16 = 0, 1
 QLORA_CB_NF4, QLORA_CB_INT4, QLORA_CB_FP4 = 0, 1, 2
 CODEBOOKS = {"nf4": QLORA_CB_NF4, "int4": QLORA_CB_INT4, "fp4": QLORA_CB_FP4}
 QLORA_OP_DOUBLE_QUANT, QLORA_OP_LINEAR_FWD, QLORA_OP_LINEAR_BWD = 0, 1, 2
-QLORA_OP_NORM_BWD = 3
+QLORA_OP_NORM_BWD, QLORA_OP_LOSS_FWD, QLORA_OP_LOSS_BWD = 3, 4, 5
 BLOCK, CHUNK, MAX_RANK = 64, 256, 128
 
 EXPORTED = ("qlora_quantize", "qlora_double_quant", "qlora_dequantize", "qlora_linear_fwd",
@@ -30,7 +30,7 @@ EXPORTED = ("qlora_quantize", "qlora_double_quant", "qlora_dequantize", "qlora_l
             "qlora_quantize_cb", "qlora_dequantize_cb", "qlora_dequantize_nodq", "qlora_codebook_levels",
             "qlora_linear_fwd_cb", "qlora_linear_bwd_cb", "qlora_merge_adapter_cb", "qlora_merge_requantize_cb",
             "qlora_silu_gate_fwd", "qlora_silu_gate_bwd", "qlora_grad_sum", "qlora_double_quant_noalloc",
-            "qlora_norm_fwd", "qlora_norm_bwd",
+            "qlora_norm_fwd", "qlora_norm_bwd", "qlora_loss_fwd", "qlora_loss_bwd",
             "qlora_workspace_size", "qlora_stream_probe",
             "qlora_status_string", "qlora_nf4_levels", "qlora_set_timing_events")
 
@@ -76,6 +76,8 @@ def _load():
     L.qlora_grad_sum.argtypes = [ctypes.POINTER(vp), i32, i64, vp, vp]
     L.qlora_norm_fwd.argtypes = [vp, st, vp, vp, vp, f32, vp, f32, i64, i64, vp, vp, vp, vp, vp]
     L.qlora_norm_bwd.argtypes = [vp, vp, st, vp, vp, vp, vp, vp, vp, f32, vp, i64, i64, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.qlora_loss_fwd.argtypes = [vp, vp, vp, i64, i64, i64, vp, vp, vp, sz, vp]
+    L.qlora_loss_bwd.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, vp, vp, vp, sz, vp]
     L.qlora_stream_probe.argtypes = [i32, i32, i32, i32, vp, vp, i64, vp]
     L.qlora_adamw_step.argtypes = [vp, vp, vp, vp, i64, i64, f32, f32, f32, f32, f32, vp, vp]
     L.qlora_workspace_size.argtypes = [st, i64, i64, i64, i32, ctypes.POINTER(sz)]
@@ -516,3 +518,58 @@ def qlora_norm_bwd(dN: Optional[torch.Tensor], dR_out: Optional[torch.Tensor], R
           _ptr(dY), _ptr(dw_pre), _ptr(dw_post), _ptr(dgate), _ptr(workspace),
           0 if workspace is None else workspace.numel())
     return dR, dY, dw_pre, dw_post, dgate
+
+
+# ---------------------------------------------------------------------------
+# Cross entropy of an output head, without kept logits
+# ---------------------------------------------------------------------------
+
+def _workspace(op: int, given: Optional[torch.Tensor], device, *sizes) -> torch.Tensor:
+    if given is None:
+        return torch.empty(workspace_size(op, *sizes), dtype=torch.uint8, device=device)
+    _want("workspace", given, torch.uint8, (given.numel(),), device)
+    return given
+
+
+def _head_shapes(H: torch.Tensor, W: torch.Tensor):
+    if H.dim() != 2 or W.dim() != 2 or H.shape[1] != W.shape[1]:
+        raise ValueError("hidden states [tokens][h] and a head [vocabulary][h] are wanted")
+    return H.shape[0], H.shape[1], W.shape[0]
+
+
+def qlora_loss_fwd(H: torch.Tensor, W: torch.Tensor, labels: torch.Tensor, loss: Optional[torch.Tensor] = None,
+                   lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """Cross entropy of softmax(H·W^T) with `labels` per token -> (loss f32 [M], lse f32 [M]).
+    Tokens whose label is outside [0, V) carry none (both 0)."""
+    M, h, V = _head_shapes(H, W)
+    dev = H.device
+    loss = torch.empty(M, dtype=torch.float32, device=dev) if loss is None else loss
+    lse = torch.empty(M, dtype=torch.float32, device=dev) if lse is None else lse
+    for name, t, dtype, shape in (("H", H, torch.bfloat16, (M, h)), ("W", W, torch.bfloat16, (V, h)),
+                                  ("labels", labels, torch.int64, (M,)), ("loss", loss, torch.float32, (M,)),
+                                  ("lse", lse, torch.float32, (M,))):
+        _want(name, t, dtype, shape, dev)
+    ws = _workspace(QLORA_OP_LOSS_FWD, workspace, dev, M, h, V)
+    _call(dev, "qlora_loss_fwd", _ptr(H), _ptr(W), _ptr(labels), M, h, V, _ptr(loss), _ptr(lse), _ptr(ws), ws.numel())
+    return loss, lse
+
+
+def qlora_loss_bwd(H: torch.Tensor, W: torch.Tensor, labels: torch.Tensor, lse: torch.Tensor, dloss: torch.Tensor,
+                   train_head: bool = False, dH: Optional[torch.Tensor] = None, dW: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None):
+    """Gradients of qlora_loss_fwd for the gradient `dloss` of each token's loss ->
+    (dH bf16 [M][h], dW bf16 [V][h], or None for a frozen head)."""
+    M, h, V = _head_shapes(H, W)
+    dev = H.device
+    dH = torch.empty(M, h, dtype=torch.bfloat16, device=dev) if dH is None else dH
+    if train_head and dW is None:
+        dW = torch.empty(V, h, dtype=torch.bfloat16, device=dev)
+    for name, t, dtype, shape in (("H", H, torch.bfloat16, (M, h)), ("W", W, torch.bfloat16, (V, h)),
+                                  ("labels", labels, torch.int64, (M,)), ("lse", lse, torch.float32, (M,)),
+                                  ("dloss", dloss, torch.float32, (M,)), ("dH", dH, torch.bfloat16, (M, h)),
+                                  ("dW", dW, torch.bfloat16, (V, h))):
+        _want(name, t, dtype, shape, dev)
+    ws = _workspace(QLORA_OP_LOSS_BWD, workspace, dev, M, h, V)
+    _call(dev, "qlora_loss_bwd", _ptr(H), _ptr(W), _ptr(labels), _ptr(lse), _ptr(dloss), M, h, V, _ptr(dH), _ptr(dW),
+          _ptr(ws), ws.numel())
+    return dH, dW

@@ -6,6 +6,7 @@
 #include "codec.h"
 #include "glue.h"
 #include "linear.h"
+#include "loss.h"
 #include "norm.h"
 #include "optim.h"
 #include "stream.h"
@@ -189,6 +190,33 @@ qlora_status_t qlora_norm_bwd(const uint16_t *dN, const void *dR_out, qlora_dtyp
                                        reinterpret_cast<hipStream_t>(stream)));
 }
 
+qlora_status_t qlora_loss_fwd(const uint16_t *H, const uint16_t *W, const int64_t *labels, int64_t M, int64_t h,
+                              int64_t V, float *loss, float *lse, void *workspace, size_t ws_bytes, void *stream) {
+  if (!H || !W || !labels || !loss || !lse || M < 1 || V < 1 || h < 1 || h % 64) return QLORA_ERR_INVALID_VALUE;
+  if (!aligned16({H, W}) || !aligned(labels, 8) || !aligned(loss, 4) || !aligned(lse, 4) || loss == lse)
+    return QLORA_ERR_INVALID_VALUE;
+  if (!loss_supported(M, h, V)) return QLORA_ERR_UNSUPPORTED;
+  if (!workspace || !aligned(workspace, 256) || ws_bytes < round256(loss_fwd_workspace(M, h, V)))
+    return QLORA_ERR_INVALID_VALUE;
+  const LossArgs a{H, W, labels, M, h, V};
+  return launch_status(launch_loss_fwd(a, loss, lse, workspace, reinterpret_cast<hipStream_t>(stream)));
+}
+
+qlora_status_t qlora_loss_bwd(const uint16_t *H, const uint16_t *W, const int64_t *labels, const float *lse,
+                              const float *dloss, int64_t M, int64_t h, int64_t V, uint16_t *dH, uint16_t *dW,
+                              void *workspace, size_t ws_bytes, void *stream) {
+  if (!H || !W || !labels || !lse || !dloss || !dH || M < 1 || V < 1 || h < 1 || h % 64)
+    return QLORA_ERR_INVALID_VALUE;
+  if (!aligned16({H, W, dH, dW}) || !aligned(labels, 8) || !aligned(lse, 4) || !aligned(dloss, 4))
+    return QLORA_ERR_INVALID_VALUE;
+  if (dH == H || dH == W || dH == dW || dW == W || dW == H) return QLORA_ERR_INVALID_VALUE;
+  if (!loss_supported(M, h, V)) return QLORA_ERR_UNSUPPORTED;
+  if (!workspace || !aligned(workspace, 256) || ws_bytes < round256(loss_bwd_workspace(M, h, V)))
+    return QLORA_ERR_INVALID_VALUE;
+  const LossArgs a{H, W, labels, M, h, V};
+  return launch_status(launch_loss_bwd(a, lse, dloss, dH, dW, workspace, reinterpret_cast<hipStream_t>(stream)));
+}
+
 qlora_status_t qlora_stream_probe(int32_t rd, int32_t wr, int32_t depth, int32_t blocks, const void *src, void *dst,
                                   int64_t n_tiles, void *stream) {
   const bool kind = (rd == 1 && wr == 0) || (rd == 4 && wr == 1) || (rd == 1 && wr == 4);
@@ -223,6 +251,11 @@ qlora_status_t qlora_workspace_size(qlora_op_t op, int64_t a, int64_t b, int64_t
     case QLORA_OP_NORM_BWD:
       if (a < 1 || b < 1 || b > kMaxNormWidth) return QLORA_ERR_INVALID_VALUE;
       *bytes = round256(norm_bwd_workspace(a, b));
+      return QLORA_OK;
+    case QLORA_OP_LOSS_FWD:
+    case QLORA_OP_LOSS_BWD:
+      if (a < 1 || c < 1 || b < 64 || b % 64 || !loss_supported(a, b, c)) return QLORA_ERR_INVALID_VALUE;
+      *bytes = round256(op == QLORA_OP_LOSS_FWD ? loss_fwd_workspace(a, b, c) : loss_bwd_workspace(a, b, c));
       return QLORA_OK;
   }
   return QLORA_ERR_INVALID_VALUE;

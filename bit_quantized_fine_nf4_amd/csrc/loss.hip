@@ -1,0 +1,282 @@
+// Softmax cross entropy of an output head over a large vocabulary without kept logits.
+//
+// For hidden states H [M][h], a head W [V][h] and labels, with z = H · W^T:
+//   lse = log(sum_v exp z_v),   loss = lse - z[label]
+//   G   = (softmax(z) - onehot(label)) * dloss,   dH = G · W,   dW = G^T · H
+// z (M x V, gigabytes) is never stored: the forward's product keeps, per tile of the
+// vocabulary, each token's maximum and sum of exponentials; the backward computes z
+// again, piece by piece of the vocabulary, turns each piece into G in bf16 and multiplies
+// it at once.  G is rounded to bf16 because it is a matrix-core operand of the two
+// gradient products; their sums are float32.
+//
+// Tokens whose label is outside [0, V) (prompt and padding tokens) carry no loss.  The
+// others are first gathered into a compact copy of H, so such tokens cost no products
+// and whatever their rows hold (NaN included) reaches nothing.  Their number is known
+// on the GPU only: launches are sized for all M tokens and the surplus workgroups leave.
+//
+// Kernels: loss_select_kernel (one workgroup: the compact list), loss_gather_kernel
+// (the copy; zeroes the skipped rows of dH), the products of loss_gemm.hip,
+// loss_finish_kernel (lse and loss from the tiles' statistics), loss_dh_kernel (sums
+// dH's partials and rounds).  Everything is added in a fixed order: no atomics.
+
+#include "loss.h"
+
+namespace ql {
+namespace {
+
+inline int64_t cdiv(int64_t x, int64_t m) { return (x + m - 1) / m; }
+
+constexpr int kSelThreads = 1024;
+
+}  // namespace
+
+// The tokens with a label in [0, V), in order: idx[i], label[i], and with `lse` the
+// compact lse and dloss.  Tokens without one get loss = lse = 0 (forward).
+__global__ __launch_bounds__(kSelThreads) void loss_select_kernel(const int64_t *labels, int64_t M, int64_t V,
+                                                                  int *count, int *idx, int *label,
+                                                                  const float *lse, const float *dloss,
+                                                                  float *c_lse, float *c_dloss, float *out_loss,
+                                                                  float *out_lse) {
+  __shared__ int sums[2][kSelThreads / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int base = 0;
+  int buf = 0;
+  for (int64_t m0 = 0; m0 < M; m0 += 4 * kSelThreads, buf ^= 1) {
+    int64_t lab[4];
+    int ok[4], mine = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t m = m0 + 4 * tid + j;
+      lab[j] = m < M ? labels[m] : -1;
+      ok[j] = lab[j] >= 0 && lab[j] < V;
+      mine += ok[j];
+    }
+    int inc = mine;  // inclusive sum over the wave
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(inc, d, 64);
+      if (lane >= d) inc += o;
+    }
+    if (lane == 63) sums[buf][wave] = inc;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kSelThreads / 64; ++w) {
+      const int s = sums[buf][w];
+      before += w < wave ? s : 0;
+      all += s;
+    }
+    int at = base + before + inc - mine;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t m = m0 + 4 * tid + j;
+      if (ok[j]) {
+        idx[at] = (int)m;
+        label[at] = (int)lab[j];
+        if (lse) {
+          c_lse[at] = lse[m];
+          c_dloss[at] = dloss[m];
+        }
+        ++at;
+      } else if (out_loss && m < M) {
+        out_loss[m] = 0.0f;
+        out_lse[m] = 0.0f;
+      }
+    }
+    base += all;
+  }
+  if (tid == 0) *count = base;
+}
+
+// Row i of the compact copy = row idx[i] of H (i < n); with dH, the rows without a label
+// become zero.  One wave per row.
+__global__ __launch_bounds__(256) void loss_gather_kernel(const uint16_t *H, int64_t M, int64_t h, const int *count,
+                                                          const int *idx, uint16_t *Hc, const int64_t *labels,
+                                                          int64_t V, uint16_t *dH) {
+  const int lane = threadIdx.x & 63;
+  const int n = *count;
+  for (int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); i < M; i += (int64_t)gridDim.x * 4) {
+    if (i < n) {
+      const u32x4 *src = reinterpret_cast<const u32x4 *>(H + (int64_t)idx[i] * h);
+      u32x4 *dst = reinterpret_cast<u32x4 *>(Hc + i * h);
+      for (int64_t c = lane; c < h / 8; c += 64) dst[c] = src[c];
+    }
+    if (dH && (labels[i] < 0 || labels[i] >= V)) {
+      u32x4 *dst = reinterpret_cast<u32x4 *>(dH + i * h);
+      for (int64_t c = lane; c < h / 8; c += 64) dst[c] = u32x4{0, 0, 0, 0};
+    }
+  }
+}
+
+// lse and loss of compact token i from the tiles' (max, sum).  One wave per token.
+__global__ __launch_bounds__(256) void loss_finish_kernel(const f32x2 *part, int64_t ldp, int tiles, const int *count,
+                                                          const int *idx, const float *zlab, float *loss, float *lse) {
+  const int lane = threadIdx.x & 63;
+  const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (i >= *count) return;
+  float mx = -__builtin_inff(), s = 0.0f;
+  for (int t = lane; t < tiles; t += 64) {
+    const f32x2 a = part[(int64_t)t * ldp + i];
+    const float m = fmaxf(mx, a[0]);
+    s = s * __expf(mx - m) + a[1] * __expf(a[0] - m);
+    mx = m;
+  }
+  float top = mx;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+  s *= mx == -__builtin_inff() ? 0.0f : __expf(mx - top);  // a lane without tiles
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d, 64);
+  if (lane == 0) {
+    const float l = top + logf(s);
+    lse[idx[i]] = l;
+    loss[idx[i]] = l - zlab[i];
+  }
+}
+
+// dH[idx[i]] = bf16(sum over the splits of part[split][i]), eight values per thread.
+__global__ __launch_bounds__(256) void loss_dh_kernel(const float *part, int splits, int64_t rows, int64_t h,
+                                                      const int *count, const int *idx, uint16_t *dH) {
+  const int64_t per = h / 8, total = (int64_t)*count * per;
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
+    const int64_t i = e / per, c = e % per * 8;
+    const float *src = part + i * h + c;
+    f32x4 a = *reinterpret_cast<const f32x4 *>(src), b = *reinterpret_cast<const f32x4 *>(src + 4);
+    for (int s = 1; s < splits; ++s) {
+      const float *q = src + (int64_t)s * rows * h;
+      a += *reinterpret_cast<const f32x4 *>(q);
+      b += *reinterpret_cast<const f32x4 *>(q + 4);
+    }
+    *reinterpret_cast<u32x4 *>(dH + (int64_t)idx[i] * h + c) =
+        u32x4{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3])};
+  }
+}
+
+namespace {
+
+// The backward's pieces of the vocabulary: G's piece [M][piece] stays near 256 MB, what
+// the last-level cache holds, so the products that follow read it from there.
+int64_t loss_piece(int64_t M, int64_t V) {
+  int64_t p = ((int64_t)1 << 27) / M / 256 * 256;
+  p = p < 4096 ? 4096 : (p > (1 << 20) ? 1 << 20 : p);
+  const int64_t all = cdiv(V, 256) * 256;
+  return p < all ? p : all;
+}
+
+// Splits of dH's sum over the vocabulary: the count in 1..16 that leaves the 256 compute
+// units idle the least, counting a split's partial sums as 4 % of a whole pass.
+int loss_splits(int64_t M, int64_t h, int64_t piece) {
+  const int64_t tiles = (M <= 64 ? 1 : cdiv(M, 256)) * cdiv(h, 256);
+  int best = 1;
+  double cost = 1e30;
+  for (int s = 1; s <= 16 && (s == 1 || piece / s >= 512); ++s) {
+    const double c = (double)cdiv(tiles * s, 256) / s + 0.04 * s * (double)tiles / 256;
+    if (c < cost - 1e-9) cost = c, best = s;
+  }
+  return best;
+}
+
+struct LossLayout {
+  size_t count, idx, label, lse, dloss, hc, stat, zlab, g, part, total;
+  int64_t piece, kper;
+  int splits;
+};
+
+LossLayout loss_layout(int64_t M, int64_t h, int64_t V, bool bwd) {
+  LossLayout L{};
+  size_t off = 0;
+  auto take = [&](size_t bytes) { const size_t at = off; off += (bytes + 255) / 256 * 256; return at; };
+  L.count = take(4);
+  L.idx = take((size_t)M * 4);
+  L.label = take((size_t)M * 4);
+  L.hc = take((size_t)M * h * 2);
+  if (!bwd) {
+    L.stat = take((size_t)cdiv(V, logit_tile_v(M)) * M * 8);
+    L.zlab = take((size_t)M * 4);
+  } else {
+    L.lse = take((size_t)M * 4);
+    L.dloss = take((size_t)M * 4);
+    L.piece = loss_piece(M, V);
+    L.splits = loss_splits(M, h, L.piece);
+    L.kper = cdiv(cdiv(L.piece, L.splits), kBlock) * kBlock;
+    L.splits = (int)cdiv(V < L.piece ? V : L.piece, L.kper);  // those that the first piece fills
+    L.g = take((size_t)M * L.piece * 2);
+    L.part = take((size_t)L.splits * M * h * 4);
+  }
+  L.total = off;
+  return L;
+}
+
+template <typename T>
+T *at(void *ws, size_t off) { return reinterpret_cast<T *>(reinterpret_cast<char *>(ws) + off); }
+
+unsigned grid4(int64_t M) { return (unsigned)(cdiv(M, 4) < 65536 ? cdiv(M, 4) : 65536); }
+
+}  // namespace
+
+bool loss_supported(int64_t M, int64_t h, int64_t V) {
+  // 32-bit offsets of 256 rows of the head, 32-bit tile numbers and thread counts
+  return h <= ((int64_t)1 << 20) && V <= ((int64_t)1 << 24) && M <= ((int64_t)1 << 24) &&
+         cdiv(M, 256) * cdiv(V, 128) < ((int64_t)1 << 24);
+}
+
+size_t loss_fwd_workspace(int64_t M, int64_t h, int64_t V) { return loss_layout(M, h, V, false).total; }
+size_t loss_bwd_workspace(int64_t M, int64_t h, int64_t V) { return loss_layout(M, h, V, true).total; }
+
+hipError_t launch_loss_fwd(const LossArgs &a, float *loss, float *lse, void *ws, hipStream_t st) {
+  const LossLayout L = loss_layout(a.M, a.h, a.V, false);
+  int *count = at<int>(ws, L.count), *idx = at<int>(ws, L.idx), *label = at<int>(ws, L.label);
+  uint16_t *Hc = at<uint16_t>(ws, L.hc);
+  hipError_t e = launch(loss_select_kernel, 1, kSelThreads, st, a.labels, a.M, a.V, count, idx, label,
+                        (const float *)nullptr, (const float *)nullptr, (float *)nullptr, (float *)nullptr, loss, lse);
+  if (e != hipSuccess) return e;
+  e = launch(loss_gather_kernel, grid4(a.M), 256, st, a.H, a.M, a.h, (const int *)count, (const int *)idx, Hc, a.labels,
+             a.V, (uint16_t *)nullptr);
+  if (e != hipSuccess) return e;
+  LogitParams p{};
+  p.W = a.W, p.H = Hc, p.count = count, p.label = label, p.h = a.h, p.v0 = 0, p.nvoc = a.V;
+  p.part = at<f32x2>(ws, L.stat), p.ldp = a.M, p.zlab = at<float>(ws, L.zlab);
+  e = launch_logit_stats(p, a.M, st);
+  if (e != hipSuccess) return e;
+  return launch(loss_finish_kernel, (unsigned)cdiv(a.M, 4), 256, st, (const f32x2 *)p.part, p.ldp, p.tiles_v,
+                (const int *)count, (const int *)idx, (const float *)p.zlab, loss, lse);
+}
+
+hipError_t launch_loss_bwd(const LossArgs &a, const float *lse, const float *dloss, uint16_t *dH, uint16_t *dW,
+                           void *ws, hipStream_t st) {
+  const LossLayout L = loss_layout(a.M, a.h, a.V, true);
+  int *count = at<int>(ws, L.count), *idx = at<int>(ws, L.idx), *label = at<int>(ws, L.label);
+  uint16_t *Hc = at<uint16_t>(ws, L.hc);
+  float *c_lse = at<float>(ws, L.lse), *c_dl = at<float>(ws, L.dloss);
+  hipError_t e = launch(loss_select_kernel, 1, kSelThreads, st, a.labels, a.M, a.V, count, idx, label, lse, dloss,
+                        c_lse, c_dl, (float *)nullptr, (float *)nullptr);
+  if (e != hipSuccess) return e;
+  e = launch(loss_gather_kernel, grid4(a.M), 256, st, a.H, a.M, a.h, (const int *)count, (const int *)idx, Hc, a.labels,
+             a.V, dH);
+  if (e != hipSuccess) return e;
+  float *part = at<float>(ws, L.part);
+  for (int64_t v0 = 0; v0 < a.V; v0 += L.piece) {
+    const int64_t nvoc = a.V - v0 < L.piece ? a.V - v0 : L.piece;
+    LogitParams p{};
+    p.W = a.W + v0 * a.h, p.H = Hc, p.count = count, p.label = label, p.h = a.h, p.v0 = v0, p.nvoc = nvoc;
+    p.lse = c_lse, p.dloss = c_dl, p.G = at<uint16_t>(ws, L.g), p.ldg = L.piece;
+    e = launch_logit_grad(p, a.M, st);
+    if (e != hipSuccess) return e;
+    HeadGradParams q{};
+    q.G = p.G, q.ldg = L.piece, q.W = p.W, q.H = Hc, q.count = count, q.h = a.h, q.nvoc = nvoc;
+    q.kper = L.kper, q.part = part, q.rows = a.M, q.add = v0 > 0;
+    // the last piece may fill fewer splits: the others' sums are whole already
+    e = launch_head_dh(q, (int)cdiv(nvoc, L.kper), a.M, st);
+    if (e != hipSuccess) return e;
+    if (dW) {
+      q.dW = dW + v0 * a.h;
+      e = launch_head_dw(q, st);
+      if (e != hipSuccess) return e;
+    }
+  }
+  const int64_t groups = cdiv(a.M * (a.h / 8), 256);
+  return launch(loss_dh_kernel, (unsigned)(groups < 8192 ? groups : 8192), 256, st, (const float *)part, L.splits, a.M,
+                a.h, (const int *)count, (const int *)idx, dH);
+}
+
+}  // namespace ql

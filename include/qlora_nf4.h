@@ -69,7 +69,9 @@ typedef enum {
   QLORA_OP_DOUBLE_QUANT = 0, /* a = number of block scales */
   QLORA_OP_LINEAR_FWD = 1,   /* a = M tokens, b = h, c = o */
   QLORA_OP_LINEAR_BWD = 2,   /* a = M tokens, b = h, c = o */
-  QLORA_OP_NORM_BWD = 3      /* a = M rows, b = h */
+  QLORA_OP_NORM_BWD = 3,     /* a = M rows, b = h */
+  QLORA_OP_LOSS_FWD = 4,     /* a = M tokens, b = h, c = V */
+  QLORA_OP_LOSS_BWD = 5      /* a = M tokens, b = h, c = V */
 } qlora_op_t;
 
 #define QLORA_BLOCK 64      /* weights per first-level scale ([MC] "2. Double quantization") */
@@ -378,6 +380,36 @@ qlora_status_t qlora_norm_bwd(const uint16_t *dN, const void *dR_out, qlora_dtyp
                               const float *gate, float alpha, const float *w_pre, int64_t M, int64_t h, void *dR,
                               uint16_t *dY, float *dw_pre, float *dw_post, float *dgate, void *workspace,
                               size_t ws_bytes, void *stream);
+
+/*
+ * Softmax cross entropy of an output head over a large vocabulary, with its gradient
+ * ([MC] "One training step", [TT] §4 "One QLoRA Training Step, End to End": forward,
+ * loss, backward).  For hidden states H [M][h] bf16, a head W [V][h] bf16 (a linear's
+ * weight order) and labels [M] int64, with z = H·W^T in float32:
+ *   lse  = log(sum_v exp(z_v))            loss = lse - z[label]
+ *   G    = (exp(z - lse) - onehot(label)) * dloss
+ *   dH   = G·W                            dW   = G^T·H
+ * z is never stored.  The forward keeps per-tile statistics; the backward computes z
+ * again in pieces of the vocabulary, each turned into bf16 G (one rounding, then
+ * float32 sums) in the workspace.  A token whose label is outside [0, V), such as
+ * -100, carries no loss: its loss and lse are 0, its dH row is 0, it adds nothing to
+ * dW, costs no products, and its H row may hold anything.  Sums run in a fixed order.
+ *  M, V >= 1, h a positive multiple of 64.  h > 2^20, M or V > 2^24, or more than
+ *  2^24 tiles of 256 tokens x 128 words are QLORA_ERR_UNSUPPORTED.
+ *  H, W, dH, dW 16-byte aligned; labels 8; loss, lse, dloss 4; workspace 256.
+ *
+ * qlora_loss_fwd  loss, lse   out, [M] float32.
+ *  workspace: qlora_workspace_size(QLORA_OP_LOSS_FWD, M, h, V, 0) bytes.
+ * qlora_loss_bwd  lse as the forward gave it; dloss [M] float32, the gradient of each
+ *  token's loss (1 / count for the mean).  dH out, [M][h] bf16.  dW out, [V][h] bf16,
+ *  or NULL: the head is frozen.  Outputs overlap nothing.
+ *  workspace: qlora_workspace_size(QLORA_OP_LOSS_BWD, M, h, V, 0) bytes.
+ */
+qlora_status_t qlora_loss_fwd(const uint16_t *H, const uint16_t *W, const int64_t *labels, int64_t M, int64_t h,
+                              int64_t V, float *loss, float *lse, void *workspace, size_t ws_bytes, void *stream);
+qlora_status_t qlora_loss_bwd(const uint16_t *H, const uint16_t *W, const int64_t *labels, const float *lse,
+                              const float *dloss, int64_t M, int64_t h, int64_t V, uint16_t *dH, uint16_t *dW,
+                              void *workspace, size_t ws_bytes, void *stream);
 
 /* Workspace bytes an entry point needs (always a multiple of 256; may be 0). */
 qlora_status_t qlora_workspace_size(qlora_op_t op, int64_t a, int64_t b, int64_t c, int32_t r,

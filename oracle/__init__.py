@@ -29,4 +29,5 @@ from .ledger import storage_bits_per_weight, storage_bytes, lora_param_count  # 
 from .optim import adamw_step  # noqa: F401
 from .glue import sigmoid, silu_gate_fwd, silu_gate_bwd, grad_sum  # noqa: F401
 from .norm import norm_fwd, norm_bwd  # noqa: F401
+from .loss import loss_fwd, loss_grad, loss_bwd  # noqa: F401
 from . import codebooks  # noqa: F401

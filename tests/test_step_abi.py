@@ -52,3 +52,37 @@ def test_norm_limits():
     for a, b in ((0, 64), (4, 0), (4, 16385)):
         with pytest.raises(nf4.QloraError):
             nf4.workspace_size(nf4.QLORA_OP_NORM_BWD, a, b)
+
+
+def loss_fwd(H=A[0], W=A[1], lab=A[2], M=4, h=64, V=100, loss=A[3], lse=A[4], ws=A[5], wb=1 << 40):
+    return lib.qlora_loss_fwd(H, W, lab, M, h, V, loss, lse, ws, wb, None)
+
+
+def loss_bwd(H=A[0], W=A[1], lab=A[2], lse=A[3], dl=A[4], M=4, h=64, V=100, dH=A[5], dW=A[6], ws=A[7], wb=1 << 40):
+    return lib.qlora_loss_bwd(H, W, lab, lse, dl, M, h, V, dH, dW, ws, wb, None)
+
+
+@pytest.mark.parametrize("call", [loss_fwd, loss_bwd])
+@pytest.mark.parametrize("bad", [
+    dict(H=None), dict(W=None), dict(lab=None), dict(lse=None), dict(M=0), dict(V=0), dict(h=0), dict(h=100),
+    dict(H=ODD), dict(W=ODD), dict(lab=ODD), dict(ws=None), dict(wb=256), dict(ws=ctypes.c_void_p(0x100010)),
+])
+def test_loss_refusals(call, bad):
+    assert call(**bad) == INV
+
+
+def test_loss_own_refusals():
+    assert loss_fwd(loss=None) == INV and loss_fwd(loss=A[4]) == INV
+    assert loss_bwd(dl=None) == INV and loss_bwd(dH=None) == INV and loss_bwd(dH=ODD) == INV
+    assert loss_bwd(dH=A[0]) == INV and loss_bwd(dH=A[6]) == INV and loss_bwd(dW=A[1]) == INV
+    for call in (loss_fwd, loss_bwd):
+        assert call(h=(1 << 20) + 64) == UNS and call(V=(1 << 24) + 1) == UNS and call(M=1 << 25) == UNS
+        assert call(M=1 << 20, V=1 << 20) == UNS      # too many tiles
+    for op in (nf4.QLORA_OP_LOSS_FWD, nf4.QLORA_OP_LOSS_BWD):
+        assert nf4.workspace_size(op, 100, 128, 1000) % 256 == 0
+        for a, b, c in ((0, 64, 10), (4, 65, 10), (4, 64, 0), (1 << 20, 64, 1 << 20)):
+            with pytest.raises(nf4.QloraError):
+                nf4.workspace_size(op, a, b, c)
+    # the backward's workspace follows a piece of the vocabulary, not the whole of it
+    small, large = (nf4.workspace_size(nf4.QLORA_OP_LOSS_BWD, 65536, 64, V) for V in (8192, 131072))
+    assert large == small
