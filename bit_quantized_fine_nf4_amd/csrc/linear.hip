@@ -426,7 +426,12 @@ __global__ __launch_bounds__(256) void lora_grad_kernel(GradProblem pa, GradProb
 #pragma unroll
     for (int u = 0; u < QCH; ++u) S.q[u] = __builtin_amdgcn_raw_buffer_load_b128(rQ, voffQ[u], sq, 0);
   };
-  auto put = [&](int buf, const Stage &S) {
+  // An odd number of Q elements ends in half a dword, and a load of the whole dword is
+  // past the view's end and reads zero: the thread that stores the last piece loads the
+  // last element (the low half: every slab starts at an even element) on its own.
+  const int64_t qn = (me - ms) * ldq;
+  const int qlast = (qn & 1) ? (int)(qn - 1 - (int64_t)(nsteps - 1) * 64 * ldq) : -1;
+  auto put = [&](int st, int buf, const Stage &S) {
 #pragma unroll
     for (int u = 0; u < PCH; ++u) *reinterpret_cast<u32x4 *>(&Ps[buf][soffP[u]]) = S.p[u];
 #pragma unroll
@@ -434,7 +439,14 @@ __global__ __launch_bounds__(256) void lora_grad_kernel(GradProblem pa, GradProb
       const int ch = tid + 256 * u;
       if (ch < 8 * ldq) {
         const int off = qtr ? (ch / qpr) * LQ + (ch % qpr) * 8 : ch * 8;
-        *reinterpret_cast<u32x4 *>(&Qs[buf][off]) = S.q[u];
+        u32x4 v = S.q[u];
+        if (qlast >= 0 && st == nsteps - 1 && ch == qlast >> 3) {
+          const uint32_t e = __builtin_amdgcn_raw_buffer_load_b16(rQ, (int)(qn - 1) * 2, 0, 0);
+#pragma unroll
+          for (int d = 0; d < 4; ++d)
+            if (d == (qlast & 7) >> 1) v[d] = e;
+        }
+        *reinterpret_cast<u32x4 *>(&Qs[buf][off]) = v;
       }
     }
   };
@@ -479,19 +491,19 @@ __global__ __launch_bounds__(256) void lora_grad_kernel(GradProblem pa, GradProb
   __builtin_amdgcn_sched_barrier(0);
   load(1, S1);
   __builtin_amdgcn_sched_barrier(0);
-  put(0, S0);
+  put(0, 0, S0);
   __syncthreads();
   for (int st = 0; st < nsteps; st += 2) {
     load(st + 2, S0);
     __builtin_amdgcn_sched_barrier(0);
     compute(0);
-    put(1, S1);
+    put(st + 1, 1, S1);
     __syncthreads();
     if (st + 1 >= nsteps) break;
     load(st + 3, S1);
     __builtin_amdgcn_sched_barrier(0);
     compute(1);
-    put(0, S0);
+    put(st + 2, 0, S0);
     __syncthreads();
   }
 
