@@ -22,7 +22,7 @@ QLORA_F32, QLORA_BF16 = 0, 1
 QLORA_CB_NF4, QLORA_CB_INT4, QLORA_CB_FP4 = 0, 1, 2
 CODEBOOKS = {"nf4": QLORA_CB_NF4, "int4": QLORA_CB_INT4, "fp4": QLORA_CB_FP4}
 QLORA_OP_DOUBLE_QUANT, QLORA_OP_LINEAR_FWD, QLORA_OP_LINEAR_BWD = 0, 1, 2
-QLORA_OP_NORM_BWD, QLORA_OP_LOSS_FWD, QLORA_OP_LOSS_BWD = 3, 4, 5
+QLORA_OP_NORM_BWD, QLORA_OP_LOSS_FWD, QLORA_OP_LOSS_BWD, QLORA_OP_LINEAR_DROPOUT = 3, 4, 5, 6
 BLOCK, CHUNK, MAX_RANK = 64, 256, 128
 
 EXPORTED = ("qlora_quantize", "qlora_double_quant", "qlora_dequantize", "qlora_linear_fwd",
@@ -31,6 +31,7 @@ EXPORTED = ("qlora_quantize", "qlora_double_quant", "qlora_dequantize", "qlora_l
             "qlora_linear_fwd_cb", "qlora_linear_bwd_cb", "qlora_merge_adapter_cb", "qlora_merge_requantize_cb",
             "qlora_silu_gate_fwd", "qlora_silu_gate_bwd", "qlora_grad_sum", "qlora_double_quant_noalloc",
             "qlora_norm_fwd", "qlora_norm_bwd", "qlora_loss_fwd", "qlora_loss_bwd",
+            "qlora_dropout", "qlora_linear_fwd_dropout", "qlora_linear_bwd_dropout",
             "qlora_workspace_size", "qlora_stream_probe",
             "qlora_status_string", "qlora_nf4_levels", "qlora_set_timing_events")
 
@@ -78,6 +79,10 @@ def _load():
     L.qlora_norm_bwd.argtypes = [vp, vp, st, vp, vp, vp, vp, vp, vp, f32, vp, i64, i64, vp, vp, vp, vp, vp, vp, sz, vp]
     L.qlora_loss_fwd.argtypes = [vp, vp, vp, i64, i64, i64, vp, vp, vp, sz, vp]
     L.qlora_loss_bwd.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, vp, vp, vp, sz, vp]
+    f64 = ctypes.c_double
+    L.qlora_dropout.argtypes = [vp, st, i64, f64, vp, vp, vp]
+    L.qlora_linear_fwd_dropout.argtypes = [W, st, vp, i64, vp, vp, i32, f32, f64, vp, vp, vp, vp, sz, vp]
+    L.qlora_linear_bwd_dropout.argtypes = [W, st, vp, vp, vp, i64, vp, vp, i32, f32, f64, vp, vp, vp, vp, vp, sz, vp]
     L.qlora_stream_probe.argtypes = [i32, i32, i32, i32, vp, vp, i64, vp]
     L.qlora_adamw_step.argtypes = [vp, vp, vp, vp, i64, i64, f32, f32, f32, f32, f32, vp, vp]
     L.qlora_workspace_size.argtypes = [st, i64, i64, i64, i32, ctypes.POINTER(sz)]
@@ -573,3 +578,81 @@ def qlora_loss_bwd(H: torch.Tensor, W: torch.Tensor, labels: torch.Tensor, lse: 
     _call(dev, "qlora_loss_bwd", _ptr(H), _ptr(W), _ptr(labels), _ptr(lse), _ptr(dloss), M, h, V, _ptr(dH), _ptr(dW),
           _ptr(ws), ws.numel())
     return dH, dW
+
+
+# ---------------------------------------------------------------------------
+# Dropout from a counter-based generator
+# ---------------------------------------------------------------------------
+
+def _rng_state(rng: torch.Tensor, device):
+    _want("rng", rng, torch.int64, (2,), device)
+    return _ptr(rng)
+
+
+def qlora_dropout(x: torch.Tensor, p: float, rng: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Inverted dropout of a float32 or bf16 tensor with probability p.  `rng` is an int64
+    GPU tensor {seed, offset}; the same state makes the same decisions (the backward is the
+    same call on the gradient), and the next use takes an offset ceil(x.numel() / 8) further."""
+    if x.dtype not in _STREAM_TYPES:
+        raise ValueError("x is float32 or bf16")
+    out = torch.empty_like(x) if out is None else out
+    _want("x", x, x.dtype, x.shape, x.device)
+    _want("out", out, x.dtype, x.shape, x.device)
+    _call(x.device, "qlora_dropout", _ptr(x), _STREAM_TYPES[x.dtype], x.numel(), float(p), _rng_state(rng, x.device),
+          _ptr(out))
+    return out
+
+
+def _drop_check(W: NF4Weight, X, T, dY, L1, L2, outs):
+    """Shapes of a linear with dropout; returns (M, r, device)."""
+    dev = X.device
+    if X.dim() != 2 or L1 is not None and (L2 is None or L1.dim() != 2):
+        raise ValueError("X [tokens][h] and factors L1 [h][r], L2 [r][o] are wanted")
+    M, r = X.shape[0], 0 if L1 is None else L1.shape[1]
+    bf = torch.bfloat16
+    for name, t, dtype, shape in (("X", X, bf, (M, W.h)), ("T", T, bf, (M, r)), ("dY", dY, bf, (M, W.o)),
+                                  ("L1", L1, bf, (W.h, r)), ("L2", L2, bf, (r, W.o)),
+                                  ("codes", W.codes, torch.uint8, (W.h * W.o // 2,))) + outs(M, r):
+        _want(name, t, dtype, shape, dev)
+    return M, r, dev
+
+
+def _drop_workspace(given, dev, M, W, r):
+    if given is None and workspace_size(QLORA_OP_LINEAR_DROPOUT, M, W.h, W.o, r) == 0:
+        return None, 0
+    ws = _workspace(QLORA_OP_LINEAR_DROPOUT, given, dev, M, W.h, W.o, r)
+    return _ptr(ws), ws.numel()
+
+
+def qlora_linear_fwd_dropout(W: NF4Weight, X: torch.Tensor, L1: Optional[torch.Tensor], L2: Optional[torch.Tensor],
+                             s: float, p: float, rng: torch.Tensor, Y: Optional[torch.Tensor] = None,
+                             T: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """The linear with dropout on its adapter's input: T = (keep * X)·L1,
+    Y = X·W_hat + s / (1 - p)·T·L2 -> (Y bf16 [M][o], T bf16 [M][r] or None)."""
+    M, r, dev = _drop_check(W, X, T, None, L1, L2, lambda M, r: (("Y", Y, torch.bfloat16, (M, W.o)),))
+    Y = torch.empty(M, W.o, dtype=torch.bfloat16, device=dev) if Y is None else Y
+    T = torch.empty(M, r, dtype=torch.bfloat16, device=dev) if T is None and r else T
+    ws, wb = _drop_workspace(workspace, dev, M, W, r)
+    _call(dev, "qlora_linear_fwd_dropout", ctypes.byref(W.as_ctypes()), W.codebook, _ptr(X), M, _ptr(L1), _ptr(L2), r,
+          float(s), float(p), _rng_state(rng, dev), _ptr(Y), _ptr(T), ws, wb)
+    return Y, T
+
+
+def qlora_linear_bwd_dropout(W: NF4Weight, X: torch.Tensor, T: Optional[torch.Tensor], dY: torch.Tensor,
+                             L1: Optional[torch.Tensor], L2: Optional[torch.Tensor], s: float, p: float,
+                             rng: torch.Tensor, dX: Optional[torch.Tensor] = None,
+                             dL1: Optional[torch.Tensor] = None, dL2: Optional[torch.Tensor] = None,
+                             workspace: Optional[torch.Tensor] = None):
+    """Backward of qlora_linear_fwd_dropout at the same generator state ->
+    (dX bf16 [M][h], dL1 f32 [h][r], dL2 f32 [r][o])."""
+    M, r, dev = _drop_check(W, X, T, dY, L1, L2, lambda M, r: (
+        ("dX", dX, torch.bfloat16, (M, W.h)), ("dL1", dL1, torch.float32, (W.h, r)),
+        ("dL2", dL2, torch.float32, (r, W.o))))
+    dX = torch.empty(M, W.h, dtype=torch.bfloat16, device=dev) if dX is None else dX
+    if r:
+        dL1 = torch.empty(W.h, r, dtype=torch.float32, device=dev) if dL1 is None else dL1
+        dL2 = torch.empty(r, W.o, dtype=torch.float32, device=dev) if dL2 is None else dL2
+    ws, wb = _drop_workspace(workspace, dev, M, W, r)
+    _call(dev, "qlora_linear_bwd_dropout", ctypes.byref(W.as_ctypes()), W.codebook, _ptr(X), _ptr(T), _ptr(dY), M,
+          _ptr(L1), _ptr(L2), r, float(s), float(p), _rng_state(rng, dev), _ptr(dX), _ptr(dL1), _ptr(dL2), ws, wb)
+    return dX, dL1, dL2

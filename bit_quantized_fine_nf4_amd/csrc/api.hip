@@ -4,6 +4,7 @@
 
 #include "../../include/qlora_nf4.h"
 #include "codec.h"
+#include "dropout.h"
 #include "glue.h"
 #include "linear.h"
 #include "loss.h"
@@ -26,6 +27,17 @@ bool aligned16(std::initializer_list<const void *> ps) {
     if (!aligned(p, 16)) return false;
   return true;
 }
+
+// 16 bits express p, below 1, and a generator state is given
+bool valid_drop(double p, const uint64_t *rng, DropState &d) {
+  if (!(p >= 0.0 && p < 1.0) || !rng || !aligned(rng, 8)) return false;
+  const double t = std::nearbyint(p * 65536.0);
+  if (t > 65535.0) return false;
+  d.rng = rng;
+  d.threshold = (uint32_t)t;
+  return true;
+}
+double drop_scale(const DropState &d) { return 65536.0 / (65536.0 - d.threshold); }
 
 inline qlora_status_t launch_status(hipError_t e) { return e == hipSuccess ? QLORA_OK : QLORA_ERR_LAUNCH; }
 
@@ -66,6 +78,60 @@ qlora_status_t qlora_nf4_levels(float out[16]) {
   if (!t) return QLORA_ERR_INTERNAL;
   for (int i = 0; i < 16; ++i) out[i] = t->level[i];
   return QLORA_OK;
+}
+
+qlora_status_t qlora_dropout(const void *x, qlora_dtype_t dtype, int64_t n, double p, const uint64_t *rng, void *out,
+                             void *stream) {
+  DropState d{};
+  if (!x || !out || n < 1 || (dtype != QLORA_F32 && dtype != QLORA_BF16) || !valid_drop(p, rng, d))
+    return QLORA_ERR_INVALID_VALUE;
+  if (!aligned16({x, out})) return QLORA_ERR_INVALID_VALUE;
+  if (n > ((int64_t)1 << 40)) return QLORA_ERR_UNSUPPORTED;
+  return launch_status(launch_dropout(x, dtype == QLORA_BF16, n, d, (float)drop_scale(d), out,
+                                      reinterpret_cast<hipStream_t>(stream)));
+}
+
+qlora_status_t qlora_linear_fwd_dropout(const qlora_nf4_weight_t *W, qlora_codebook_t codebook, const uint16_t *X,
+                                        int64_t M, const uint16_t *L1, const uint16_t *L2, int32_t r, float s,
+                                        double p, const uint64_t *rng, uint16_t *Y, uint16_t *T, void *workspace,
+                                        size_t ws_bytes, void *stream) {
+  DropState d{};
+  if (!valid_drop(p, rng, d)) return QLORA_ERR_INVALID_VALUE;
+  if (r == 0)
+    return qlora_linear_fwd_cb(W, codebook, X, M, L1, L2, r, s, Y, T, workspace, ws_bytes, stream);
+  if (!valid_weight(W, codebook) || !X || !Y || M < 1 || M > (int64_t(1) << 31)) return QLORA_ERR_INVALID_VALUE;
+  if (r < 0 || r > QLORA_MAX_RANK || !L1 || !L2 || !T) return QLORA_ERR_INVALID_VALUE;
+  if (!aligned16({X, Y, L1, L2, T})) return QLORA_ERR_INVALID_VALUE;
+  const size_t need = round256(linear_drop_workspace(M, W->h, W->o, r));
+  if (!workspace || ws_bytes < need || !aligned(workspace, 256)) return QLORA_ERR_INVALID_VALUE;
+  const Nf4Tables *t = host_tables(codebook);
+  if (!t) return QLORA_ERR_INTERNAL;
+  const LinearArgs a{W->codes, W->qabsmax, W->scale2, W->mean, W->h, W->o, M, r, (float)(s * drop_scale(d))};
+  return launch_status(
+      launch_linear_fwd_drop(a, d, X, L1, L2, Y, T, workspace, *t, reinterpret_cast<hipStream_t>(stream)));
+}
+
+qlora_status_t qlora_linear_bwd_dropout(const qlora_nf4_weight_t *W, qlora_codebook_t codebook, const uint16_t *X,
+                                        const uint16_t *T, const uint16_t *dY, int64_t M, const uint16_t *L1,
+                                        const uint16_t *L2, int32_t r, float s, double p, const uint64_t *rng,
+                                        uint16_t *dX, float *dL1, float *dL2, void *workspace, size_t ws_bytes,
+                                        void *stream) {
+  DropState d{};
+  if (!valid_drop(p, rng, d)) return QLORA_ERR_INVALID_VALUE;
+  if (r == 0)
+    return qlora_linear_bwd_cb(W, codebook, X, T, dY, M, L1, L2, r, s, dX, dL1, dL2, workspace, ws_bytes, stream);
+  if (!valid_weight(W, codebook) || !X || !T || !dY || !dX || M < 1 || M > (int64_t(1) << 31))
+    return QLORA_ERR_INVALID_VALUE;
+  if (r < 0 || r > QLORA_MAX_RANK || !L1 || !L2 || !dL1 || !dL2) return QLORA_ERR_INVALID_VALUE;
+  if (!aligned16({X, T, dY, dX, L1, L2, dL1, dL2})) return QLORA_ERR_INVALID_VALUE;
+  const size_t need = round256(linear_drop_workspace(M, W->h, W->o, r));
+  if (!workspace || ws_bytes < need || !aligned(workspace, 256)) return QLORA_ERR_INVALID_VALUE;
+  if (!linear_drop_supported(M, W->h, W->o, r)) return QLORA_ERR_UNSUPPORTED;
+  const Nf4Tables *t = host_tables(codebook);
+  if (!t) return QLORA_ERR_INTERNAL;
+  const LinearArgs a{W->codes, W->qabsmax, W->scale2, W->mean, W->h, W->o, M, r, (float)(s * drop_scale(d))};
+  return launch_status(launch_linear_bwd_drop(a, d, X, T, dY, L1, L2, dX, dL1, dL2, workspace, *t,
+                                              reinterpret_cast<hipStream_t>(stream)));
 }
 
 qlora_status_t qlora_merge_adapter_cb(const qlora_nf4_weight_t *W, qlora_codebook_t codebook, const uint16_t *L1,
@@ -247,6 +313,10 @@ qlora_status_t qlora_workspace_size(qlora_op_t op, int64_t a, int64_t b, int64_t
       if (a < 1 || b < 64 || c < 64 || r < 0 || r > QLORA_MAX_RANK) return QLORA_ERR_INVALID_VALUE;
       *bytes = round256(op == QLORA_OP_LINEAR_FWD ? linear_fwd_workspace(a, b, c, r)
                                                   : linear_bwd_workspace(a, b, c, r));
+      return QLORA_OK;
+    case QLORA_OP_LINEAR_DROPOUT:
+      if (a < 1 || b < 64 || c < 64 || r < 0 || r > QLORA_MAX_RANK) return QLORA_ERR_INVALID_VALUE;
+      *bytes = round256(linear_drop_workspace(a, b, c, r));
       return QLORA_OK;
     case QLORA_OP_NORM_BWD:
       if (a < 1 || b < 1 || b > kMaxNormWidth) return QLORA_ERR_INVALID_VALUE;

@@ -2,6 +2,7 @@
 #pragma once
 
 #include "common.h"
+#include "dropout.h"
 
 namespace ql {
 
@@ -32,6 +33,9 @@ struct GemmParams {
   int64_t ldc;
   int tiles_m, tiles_n;
   float level[16];
+  // dX of a linear with dropout on its adapter's input: the LoRA term alone is masked,
+  // by the element's place in dX
+  DropState drop;
 };
 
 // Output tile (tm, tn) of workgroup `bid`.  The dispatcher deals workgroups to the
@@ -54,8 +58,25 @@ __device__ inline void gemm_tile_of(int bid, int tiles_m, int tiles_n, int band,
 }
 
 hipError_t launch_nf4_gemm(GemmParams &gp, bool trans, hipStream_t st);
+// dX with the LoRA term masked by gp.drop
+hipError_t launch_nf4_gemm_dx_drop(GemmParams &gp, hipStream_t st);
 // 256 x bn tiles (bn = 256 or 128) with four waves that decode B in registers, both
 // directions (nf4_gemm_wide.hip)
 hipError_t launch_nf4_gemm_wide(GemmParams &gp, bool trans, int bn, hipStream_t st);
+hipError_t launch_nf4_gemm_wide_dx_drop(GemmParams &gp, hipStream_t st);  // 256 x 256 tiles
+
+// Keep bits of a BM x BN tile of dX (origin m0, n0; N the matrix width, a multiple of
+// 64), in LDS as words[column / 32][row]: bit c of a word is column 32 w + c.  Each
+// thread makes whole bytes (eight elements, one generator call).
+template <int BM, int BN, int NT>
+QL_DEV void keep_tile(uint32_t *words, const DropState &d, int64_t m0, int64_t n0, int64_t N, int tid) {
+  const uint64_t seed = d.rng[0], offset = d.rng[1];
+  for (int i = tid; i < BM * BN / 8; i += NT) {
+    const int row = i / (BN / 8), c8 = i % (BN / 8);
+    const uint64_t block = (uint64_t)(m0 + row) * (uint64_t)(N >> 3) + (uint64_t)((n0 >> 3) + c8);
+    reinterpret_cast<uint8_t *>(words)[((c8 >> 2) * BM + row) * 4 + (c8 & 3)] =
+        (uint8_t)keep_bits(seed, offset + block, d.threshold);
+  }
+}
 
 }  // namespace ql

@@ -2,6 +2,7 @@
 #pragma once
 
 #include "common.h"
+#include "dropout.h"
 
 namespace ql {
 
@@ -33,5 +34,15 @@ hipError_t launch_linear_fwd(const LinearArgs &a, const uint16_t *X, const uint1
 hipError_t launch_linear_bwd(const LinearArgs &a, const uint16_t *X, const uint16_t *T, const uint16_t *dY,
                              const uint16_t *L1, const uint16_t *L2, uint16_t *dX, float *dL1, float *dL2,
                              void *ws, const Nf4Tables &tab, hipStream_t st);
+
+// The linear with dropout on its adapter's input; a.s already holds s / (1 - p).
+size_t linear_drop_workspace(int64_t M, int64_t h, int64_t o, int r);  // enough for either direction
+bool linear_drop_supported(int64_t M, int64_t h, int64_t o, int r);
+hipError_t launch_linear_fwd_drop(const LinearArgs &a, const DropState &d, const uint16_t *X, const uint16_t *L1,
+                                  const uint16_t *L2, uint16_t *Y, uint16_t *T, void *ws, const Nf4Tables &tab,
+                                  hipStream_t st);
+hipError_t launch_linear_bwd_drop(const LinearArgs &a, const DropState &d, const uint16_t *X, const uint16_t *T,
+                                  const uint16_t *dY, const uint16_t *L1, const uint16_t *L2, uint16_t *dX,
+                                  float *dL1, float *dL2, void *ws, const Nf4Tables &tab, hipStream_t st);
 
 }  // namespace ql

@@ -33,6 +33,9 @@
 //                        and dL2 [r][o]; both run before the dX GEMM on the
 //                        caller's stream (lora_gradp_kernel: r <= 16 in one
 //                        pass, 32- or 64-wide tiles over every token)
+//   drop_grad_kernel     dL1 with dropout on the adapter's input (below); the
+//                        rank-r kernels, the dX kernels and the few-token dX
+//                        finish have forms that make the same decisions
 
 #include "linear.h"
 #include "gemm.h"
@@ -120,6 +123,10 @@ struct RankParams {
   int64_t h;
   int ldp;
   uint16_t *L1p;
+  // dropout: the unrounded sums as well (backward; [M][16 NT], nullptr: not wanted), and
+  // the state that drops elements of A (the DROP kernels)
+  float *out32;
+  DropState drop;
 };
 
 constexpr int kRankRows = 64;  // rows per workgroup: 16 per wave
@@ -155,8 +162,11 @@ QL_DEV void rank_extras(const RankParams &p, int64_t gt, int64_t gn) {
 // L1 row starts on a 16-byte boundary and the chunk copies in 16-byte pieces
 // (otherwise element by element).  !KN: the factor is L2 [r][ldb] (k-contiguous).
 // Either way a chunk of the factor is staged once in LDS for all four waves.
-template <int NT, bool KN, bool VEC>
+// DROP (KN only): A's dropped elements are zeroed as they enter the product; a fragment
+// is eight consecutive elements of a row, one generator call.
+template <int NT, bool KN, bool VEC, bool DROP>
 __global__ __launch_bounds__(256) void lora_rank_kernel(RankParams p) {
+  static_assert(KN || !DROP, "dropout is on the forward's X");
   constexpr int RP = NT * 16;
   constexpr int LDB = RP + 8;  // KN tile [64 k][LDB]: row stride of the transposing reads
   constexpr int LDK = 64 + 8;  // NK tile [RP q][LDK]: row stride of the 16-byte fragment reads
@@ -229,9 +239,15 @@ __global__ __launch_bounds__(256) void lora_rank_kernel(RankParams p) {
     }
   };
   const int trow = i16 >> 2, tcol = (i16 & 3) * 4;
-  auto compute = [&](int buf, const Chunk &C) {
+  uint64_t seed = 0, ctr = 0;  // of the lane's first fragment
+  if constexpr (DROP) {
+    seed = p.drop.rng[0];
+    ctr = p.drop.rng[1] + (uint64_t)((m0 + 16 * wave + i16) * (p.K >> 3) + (k0 >> 3) + g);
+  }
+  auto compute = [&](int c, int buf, Chunk &C) {
 #pragma unroll
-    for (int sub = 0; sub < 2; ++sub)
+    for (int sub = 0; sub < 2; ++sub) {
+      if constexpr (DROP) C.a[sub] = drop8(C.a[sub], seed, ctr + (uint64_t)(8 * c + 4 * sub), p.drop.threshold);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         u32x4 b;
@@ -243,6 +259,7 @@ __global__ __launch_bounds__(256) void lora_rank_kernel(RankParams p) {
         }
         acc[t] = mfma16(C.a[sub], b, acc[t]);
       }
+    }
   };
 
   // Loads run kDepth chunks ahead in a ring of kDepth + 1 register stages (one
@@ -264,7 +281,7 @@ __global__ __launch_bounds__(256) void lora_rank_kernel(RankParams p) {
       const int c = c0 + u;
       load(c + kDepth, C[(u + kDepth) % kRing]);
       __builtin_amdgcn_sched_barrier(0);
-      compute(u & 1, C[u]);
+      compute(c, u & 1, C[u]);
       put(c + 1, (u + 1) & 1, C[(u + 1) % kRing]);
       __syncthreads();
     }
@@ -292,6 +309,7 @@ __global__ __launch_bounds__(256) void lora_rank_kernel(RankParams p) {
       const int64_t m = m0 + row;
       if (p.out1 && q < p.ld1) p.out1[m * p.ld1 + q] = q < r ? to_bf16(acc[t][v]) : (uint16_t)0;
       if (p.out2 && q < p.ld2) p.out2[m * p.ld2 + q] = q < r ? to_bf16(p.s * acc[t][v]) : (uint16_t)0;
+      if (p.out32) p.out32[m * RP + q] = q < r ? acc[t][v] : 0.0f;
     }
   for (int q = RP + i16; q < W; q += 16)  // columns past the rank tiles: zero
 #pragma unroll
@@ -332,6 +350,7 @@ __global__ __launch_bounds__(256) void lora_rank_reduce_kernel(RankParams p) {
     }
     if (p.out1 && q < p.ld1) p.out1[m * p.ld1 + q] = q < p.r ? to_bf16(sum) : (uint16_t)0;
     if (p.out2 && q < p.ld2) p.out2[m * p.ld2 + q] = q < p.r ? to_bf16(p.s * sum) : (uint16_t)0;
+    if (p.out32 && q < RP) p.out32[m * RP + q] = sum;
   }
   rank_extras(p, gt, gn);
 }
@@ -616,8 +635,9 @@ constexpr int kP16PastEnd = 0x7FFF0000;
 // transposing reads; an L2 chunk (16 rows of 64 k, rows past r reading as zero) into
 // rows padded to 72 elements, read back as each lane's 8 consecutive k.  Outputs as
 // lora_rank_kernel's.
-template <bool KN, bool VEC, int ROWS>
+template <bool KN, bool VEC, int ROWS, bool DROP>
 __global__ __launch_bounds__(kP16Threads) void lora_rank16_kernel(RankParams p) {
+  static_assert(KN || !DROP, "dropout is on the forward's X");
   constexpr int LDB = 24;  // KN tile [64 k][LDB]
   constexpr int LDK = 72;  // L2 tile [16 q][LDK]
   static_assert(16 * LDK <= 64 * LDB, "both tiles fit the wave's LDS area");
@@ -689,9 +709,16 @@ __global__ __launch_bounds__(kP16Threads) void lora_rank16_kernel(RankParams p) 
   };
   const int trow = i16 >> 2, tcol = (i16 & 3) * 4;
   f32x4 acc = f32x4{0, 0, 0, 0};
-  auto compute = [&](const Chunk &C) {
+  uint64_t seed = 0, ctr = 0;
+  if constexpr (DROP) {
+    seed = p.drop.rng[0];
+    ctr = p.drop.rng[1] + (uint64_t)((m0 + i16) * (p.K >> 3) + g);
+  }
+  auto compute = [&](int j, Chunk &C) {
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub) {
+      if constexpr (DROP)
+        C.a[sub] = drop8(C.a[sub], seed, ctr + (uint64_t)(8 * (wave + kP16Waves * j) + 4 * sub), p.drop.threshold);
       u32x4 b;
       if constexpr (KN) {
         const uint16_t *lo = bt + (32 * sub + 8 * g + trow) * LDB + tcol;
@@ -713,7 +740,7 @@ __global__ __launch_bounds__(kP16Threads) void lora_rank16_kernel(RankParams p) 
     for (int u = 0; u < kRing; ++u) {
       load(j0 + u + kDepth, C[(u + kDepth) % kRing]);
       put(C[u]);
-      compute(C[u]);
+      compute(j0 + u, C[u]);
     }
   }
 
@@ -730,6 +757,7 @@ __global__ __launch_bounds__(kP16Threads) void lora_rank16_kernel(RankParams p) 
       const int64_t m = m0 + row;
       if (p.out1 && q < p.ld1) p.out1[m * p.ld1 + q] = q < r ? to_bf16(sum) : (uint16_t)0;
       if (p.out2 && q < p.ld2) p.out2[m * p.ld2 + q] = q < r ? to_bf16(p.s * sum) : (uint16_t)0;
+      if (p.out32) p.out32[m * 16 + q] = q < r ? sum : 0.0f;
     }
   }
   const int W = p.ld1 > p.ld2 ? p.ld1 : p.ld2;
@@ -897,6 +925,133 @@ __global__ __launch_bounds__(kP16Threads) void lora_gradp_kernel(GradProblem pa,
 }
 
 // ---------------------------------------------------------------------------
+// dL1 = s·(keep ⊙ X)^T·U with dropout on the adapter's input.  A workgroup owns 128
+// values of i (columns of X), every rank column and a token range, walked in 64-token
+// slabs, as lora_grad_kernel does: X comes back from LDS through transposing reads.
+// X's pieces are masked on their way into LDS, one generator call per 16-byte piece and
+// every piece in one workgroup only.  U comes as the float32 sums of the rank-r product
+// and is split into three bf16 parts (U = hi + mid + lo to 2^-26), each a product of its
+// own on the same accumulators: one bf16 U alone would leave dL1, a float32 result, with
+// 2^-9 errors.  The product is bound by reading X, not by the matrix cores.  With one
+// token split the kernel scales by s and stores; otherwise lora_grad_reduce_kernel adds
+// the splits in order.
+// ---------------------------------------------------------------------------
+QL_DEV void split3(float x, float &hi, float &mid, float &lo) {
+  hi = bf16_lo(pack_bf16x2(x, 0.0f));
+  mid = bf16_lo(pack_bf16x2(x - hi, 0.0f));
+  lo = (x - hi) - mid;
+}
+
+template <int NT>
+__global__ __launch_bounds__(256) void drop_grad_kernel(GradProblem pr, const float *U, DropState drop, int rq, float s,
+                                                        int64_t M, int64_t mchunk, int64_t prows,
+                                                        float *__restrict__ part) {
+  constexpr int RP = NT * 16;
+  constexpr int LP = kGradTile + 8, LQ = RP + 8;
+  constexpr int PCH = 64 * kGradTile / 8 / 256;  // 16-byte pieces of X per thread and slab (4)
+  constexpr int QCH = 64 * RP / 4 / 256;         // 16-byte pieces of U per thread and slab (NT)
+  __shared__ __attribute__((aligned(16))) uint16_t Ps[2][64 * LP];
+  __shared__ __attribute__((aligned(16))) uint16_t Qs[3][64 * LQ];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int g = lane >> 4, c16 = lane & 15;
+  const int64_t i0 = (int64_t)blockIdx.x * kGradTile;
+  const int64_t ms = (int64_t)blockIdx.y * mchunk;
+  const int64_t me = ms + mchunk < M ? ms + mchunk : M;
+  const int nsteps = (int)((me - ms + 63) / 64);
+  const int64_t ldp = pr.ldp;
+  const auto rP = gv_rsrc(pr.P + ms * ldp + i0, (me - ms) * ldp * 2 - i0 * 2);
+  const auto rQ = gv_rsrc(U + ms * RP, (me - ms) * RP * 4);
+  const uint64_t seed = drop.rng[0], offset = drop.rng[1];
+  int voffP[PCH], soffP[PCH];
+  uint64_t ctr[PCH];
+#pragma unroll
+  for (int u = 0; u < PCH; ++u) {
+    const int ch = tid + 256 * u, row = ch >> 4, col8 = ch & 15;
+    voffP[u] = (int)((row * ldp + col8 * 8) * 2);
+    soffP[u] = row * LP + col8 * 8;
+    ctr[u] = offset + (uint64_t)((ms + row) * (ldp >> 3) + (i0 >> 3) + col8);
+  }
+  f32x4 acc[2][NT];
+#pragma unroll
+  for (int a = 0; a < 2; ++a)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[a][t] = f32x4{0, 0, 0, 0};
+  u32x4 P[PCH];
+  f32x4 Q[QCH];
+  auto load = [&](int st) {
+    const int sp = __builtin_amdgcn_readfirstlane((int)(st * 64 * ldp * 2));
+    const int sq = __builtin_amdgcn_readfirstlane(st * 64 * RP * 4);
+#pragma unroll
+    for (int u = 0; u < PCH; ++u) P[u] = __builtin_amdgcn_raw_buffer_load_b128(rP, voffP[u], sp, 0);
+#pragma unroll
+    for (int u = 0; u < QCH; ++u)
+      Q[u] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rQ, (tid + 256 * u) * 16, sq, 0));
+  };
+  auto put_p = [&](int st, int buf) {
+#pragma unroll
+    for (int u = 0; u < PCH; ++u)
+      *reinterpret_cast<u32x4 *>(&Ps[buf][soffP[u]]) =
+          drop8(P[u], seed, ctr[u] + (uint64_t)st * (uint64_t)(64 * (ldp >> 3)), drop.threshold);
+  };
+  auto put_q = [&]() {
+#pragma unroll
+    for (int u = 0; u < QCH; ++u) {
+      const int e = 4 * (tid + 256 * u), off = (e / RP) * LQ + e % RP;
+      float p[3][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) split3(Q[u][i], p[0][i], p[1][i], p[2][i]);
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        *reinterpret_cast<u32x2 *>(&Qs[k][off]) = u32x2{pack_bf16x2(p[k][0], p[k][1]), pack_bf16x2(p[k][2], p[k][3])};
+    }
+  };
+  const int trow = c16 >> 2, tcol = (c16 & 3) * 4;
+  auto compute = [&](int buf) {
+#pragma unroll
+    for (int mk = 0; mk < 64; mk += 32) {
+      u32x4 af[2];
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        const uint16_t *lo = &Ps[buf][(mk + 8 * g + trow) * LP + wave * 32 + 16 * a + tcol];
+        af[a] = tr_pair(lo, lo + 4 * LP);
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          const uint16_t *lo = &Qs[k][(mk + 8 * g + trow) * LQ + 16 * t + tcol];
+          const u32x4 bq = tr_pair(lo, lo + 4 * LQ);
+#pragma unroll
+          for (int a = 0; a < 2; ++a) acc[a][t] = mfma16(af[a], bq, acc[a][t]);
+        }
+    }
+  };
+  load(0);
+  for (int st = 0; st < nsteps; ++st) {
+    put_p(st, st & 1);
+    put_q();
+    load(st + 1);  // past the range: zeros, never used
+    __syncthreads();
+    compute(st & 1);
+    __syncthreads();  // U's parts are overwritten next
+  }
+  // D layout: lane (q = 16t + c16, g) holds rows i = 4g + v of each 16-row tile
+  float *out = gridDim.y > 1 ? part + (int64_t)blockIdx.y * prows * RP : pr.out;
+#pragma unroll
+  for (int a = 0; a < 2; ++a)
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int64_t i = i0 + wave * 32 + 16 * a + 4 * g + v;
+        const int q = t * 16 + c16;
+        if (i >= pr.I) continue;
+        if (gridDim.y > 1) out[i * RP + q] = acc[a][t][v];
+        else if (q < rq) out[i * rq + q] = s * acc[a][t][v];
+      }
+}
+
+// ---------------------------------------------------------------------------
 // Host side: split choices (shared by workspace sizing and launches), launches.
 // ---------------------------------------------------------------------------
 namespace {
@@ -1013,19 +1168,21 @@ BwdLayout bwd_layout(int64_t M, int64_t h, int64_t o, int r) {
 template <typename T>
 T *at(void *ws, size_t off) { return reinterpret_cast<T *>(reinterpret_cast<char *>(ws) + off); }
 
+// DROP: dropout on the forward's X (kn)
+template <bool DROP = false>
 hipError_t rank_r(RankParams &rp, bool kn, int RP16, float *part, hipStream_t st) {
   if (RP16 == 16) {
     // 8-row workgroups while 16-row ones would number fewer than the compute units
     if (cdiv(rp.M, 16) < 256) {
       const unsigned grid = (unsigned)cdiv(rp.M, 8);
-      if (!kn) return launch(lora_rank16_kernel<false, true, 8>, grid, kP16Threads, st, rp);
-      return rp.r % 8 == 0 ? launch(lora_rank16_kernel<true, true, 8>, grid, kP16Threads, st, rp)
-                           : launch(lora_rank16_kernel<true, false, 8>, grid, kP16Threads, st, rp);
+      if (!kn) return launch(lora_rank16_kernel<false, true, 8, false>, grid, kP16Threads, st, rp);
+      return rp.r % 8 == 0 ? launch(lora_rank16_kernel<true, true, 8, DROP>, grid, kP16Threads, st, rp)
+                           : launch(lora_rank16_kernel<true, false, 8, DROP>, grid, kP16Threads, st, rp);
     }
     const unsigned grid = (unsigned)cdiv(rp.M, 16);
-    if (!kn) return launch(lora_rank16_kernel<false, true, 16>, grid, kP16Threads, st, rp);
-    return rp.r % 8 == 0 ? launch(lora_rank16_kernel<true, true, 16>, grid, kP16Threads, st, rp)
-                         : launch(lora_rank16_kernel<true, false, 16>, grid, kP16Threads, st, rp);
+    if (!kn) return launch(lora_rank16_kernel<false, true, 16, false>, grid, kP16Threads, st, rp);
+    return rp.r % 8 == 0 ? launch(lora_rank16_kernel<true, true, 16, DROP>, grid, kP16Threads, st, rp)
+                         : launch(lora_rank16_kernel<true, false, 16, DROP>, grid, kP16Threads, st, rp);
   }
   const RankSplit rs = rank_split(rp.M, rp.K);
   rp.ks = rs.ks;
@@ -1037,9 +1194,9 @@ hipError_t rank_r(RankParams &rp, bool kn, int RP16, float *part, hipStream_t st
   switch (RP16 / 16) {
 #define QL_RK(NT)                                                                              \
   case NT:                                                                                     \
-    e = !kn ? launch(lora_rank_kernel<NT, false, true>, grid, 256, st, rp)                     \
-            : (vec ? launch(lora_rank_kernel<NT, true, true>, grid, 256, st, rp)               \
-                   : launch(lora_rank_kernel<NT, true, false>, grid, 256, st, rp));           \
+    e = !kn ? launch(lora_rank_kernel<NT, false, true, false>, grid, 256, st, rp)                     \
+            : (vec ? launch(lora_rank_kernel<NT, true, true, DROP>, grid, 256, st, rp)               \
+                   : launch(lora_rank_kernel<NT, true, false, DROP>, grid, 256, st, rp));           \
     if (e == hipSuccess && rs.ks > 1) {                                                        \
       int64_t rg = cdiv(rp.M * (rp.ld1 > rp.ld2 ? rp.ld1 : rp.ld2), 256);                      \
       rg = rg > 2048 ? 2048 : rg;                                                              \
@@ -1329,7 +1486,7 @@ __global__ __launch_bounds__(kGvmThreads) void nf4_gemv_dx_kernel(GvdParams p) {
 // meet in LDS in a fixed order.
 __global__ __launch_bounds__(256) void gemv_dx_finish_kernel(const float *part, int chunks, int M, int64_t h,
                                                              const uint16_t *sU, int ldsu, const uint16_t *L1,
-                                                             int r, uint16_t *dX, int64_t ldx) {
+                                                             int r, uint16_t *dX, int64_t ldx, DropState drop) {
   __shared__ float red[4][64][9];
   const int64_t groups = h / 8;
   const int64_t cg = (groups + 63) / 64;
@@ -1376,8 +1533,11 @@ __global__ __launch_bounds__(256) void gemv_dx_finish_kernel(const float *part, 
 #pragma unroll
       for (int i = 0; i < 8; ++i) t[i] += su * bf16_lo(L1[(k + i) * r + q]);
     }
+    // dropout on the adapter's input (rng set): its gradient passes where X was kept
+    const uint32_t keep =
+        drop.rng ? keep_bits(drop.rng[0], drop.rng[1] + (uint64_t)(m * (h >> 3) + grp), drop.threshold) : 0xFFu;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += t[i];
+    for (int i = 0; i < 8; ++i) v[i] += (keep >> i) & 1u ? t[i] : 0.0f;
   }
   *reinterpret_cast<u32x4 *>(dX + (int64_t)m * ldx + k) =
       u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
@@ -1413,8 +1573,11 @@ int64_t linear_bwd_token_splits(int64_t M, int64_t h, int64_t o) {
   return grad_split(M, h + o, h > o ? h : o).S;
 }
 
-hipError_t launch_linear_fwd(const LinearArgs &a, const uint16_t *X, const uint16_t *L1, const uint16_t *L2,
-                             uint16_t *Y, uint16_t *T, void *ws, const Nf4Tables &tab, hipStream_t st) {
+namespace {
+
+// drop: dropout on the adapter's input (nullptr: none)
+hipError_t linear_fwd(const LinearArgs &a, const uint16_t *X, const uint16_t *L1, const uint16_t *L2, uint16_t *Y,
+                      uint16_t *T, void *ws, const Nf4Tables &tab, hipStream_t st, const DropState *drop) {
   const FwdLayout L = fwd_layout(a.M, a.h, a.o, a.r);
   uint16_t *sT = nullptr;
   if (a.r > 0) {
@@ -1424,7 +1587,9 @@ hipError_t launch_linear_fwd(const LinearArgs &a, const uint16_t *X, const uint1
     rp.A = X; rp.lda = a.h; rp.M = a.M; rp.K = a.h;
     rp.B = L1; rp.ldb = a.r; rp.r = a.r; rp.s = a.s;
     rp.out1 = T; rp.ld1 = a.r; rp.out2 = sT; rp.ld2 = L.RP64;
-    const hipError_t e = rank_r(rp, true, L.RP16, at<float>(ws, L.off_tp), st);
+    if (drop) rp.drop = *drop;
+    const hipError_t e = drop ? rank_r<true>(rp, true, L.RP16, at<float>(ws, L.off_tp), st)
+                              : rank_r(rp, true, L.RP16, at<float>(ws, L.off_tp), st);
     if (e != hipSuccess) return e;
   }
   if (a.M <= 16 && gemv_fits(a)) {
@@ -1450,6 +1615,13 @@ hipError_t launch_linear_fwd(const LinearArgs &a, const uint16_t *X, const uint1
   fill_levels(gp.level, tab);
   TimedLaunch tl(0, st);
   return launch_nf4_gemm(gp, false, st);
+}
+
+}  // namespace
+
+hipError_t launch_linear_fwd(const LinearArgs &a, const uint16_t *X, const uint16_t *L1, const uint16_t *L2,
+                             uint16_t *Y, uint16_t *T, void *ws, const Nf4Tables &tab, hipStream_t st) {
+  return linear_fwd(a, X, L1, L2, Y, T, ws, tab, st, nullptr);
 }
 
 hipError_t launch_linear_bwd(const LinearArgs &a, const uint16_t *X, const uint16_t *T, const uint16_t *dY,
@@ -1498,7 +1670,7 @@ hipError_t launch_linear_bwd(const LinearArgs &a, const uint16_t *X, const uint1
     }
     const int64_t cg = (a.h / 8 + 63) / 64;
     return launch(gemv_dx_finish_kernel, (unsigned)(a.M * cg), 256, st, (const float *)vp.part, L.dxc, (int)a.M,
-                  a.h, (const uint16_t *)sU, L.RP64, L1, a.r, dX, a.h);
+                  a.h, (const uint16_t *)sU, L.RP64, L1, a.r, dX, a.h, DropState{nullptr, 0});
   }
   GemmParams gp{};
   gp.A = dY; gp.lda = a.o;
@@ -1520,6 +1692,130 @@ hipError_t launch_linear_bwd(const LinearArgs &a, const uint16_t *X, const uint1
   }
   TimedLaunch tl(1, st);
   return launch_nf4_gemm(gp, true, st);
+}
+
+// ---- the linear with dropout on its adapter's input --------------------------
+// T = (keep ⊙ X)·L1, Y = X·W_hat + s'·T·L2, dX = dY·W_hat^T + s'·keep ⊙ (U·L1^T),
+// dL1 = s'·(keep ⊙ X)^T·U, dL2 = s'·T^T·dY with s' = s / (1 - p): the scale is in s', so
+// that dropping an element is exact.
+
+namespace {
+
+struct DropLayout {
+  int RP16, RP64, dxc;
+  Split s1, s2;  // token splits of dL1 and dL2
+  size_t off_u, off_su, off_l1p, off_g1, off_g2, off_up, off_dxp, total;
+};
+
+DropLayout drop_layout(int64_t M, int64_t h, int64_t o, int r) {
+  DropLayout L{};
+  size_t off = 0;
+  auto take = [&](size_t bytes) { size_t at = off; off += rup((int64_t)bytes, 256); return at; };
+  L.RP16 = (int)rup(r, 16);
+  L.RP64 = (int)rup(r, 64);
+  if (M <= 16) {
+    L.dxc = gemv_dx_chunks(h, o);
+    L.off_dxp = take((size_t)L.dxc * M * h * 4);
+  }
+  // a split's rows of X, U (float32), dY and T stay within 32-bit offsets
+  L.s1 = grad_split(M, h, h > 2 * L.RP16 ? h : 2 * L.RP16);
+  L.s2 = grad_split(M, o, o > L.RP16 ? o : L.RP16);
+  L.off_u = take((size_t)M * L.RP16 * 4);
+  L.off_su = take((size_t)M * L.RP64 * 2);
+  L.off_l1p = take((size_t)h * L.RP64 * 2);
+  L.off_g1 = take(L.s1.S > 1 ? (size_t)L.s1.S * h * L.RP16 * 4 : 0);
+  L.off_g2 = take(grad_one_pass(M, 0, o, L.RP16) ? 0 : (size_t)L.s2.S * o * L.RP16 * 4);
+  L.off_up = take(rank_partial_bytes(M, o, L.RP16));
+  L.total = off;
+  return L;
+}
+
+hipError_t drop_grad(const GradProblem &pr, const float *U, const DropState &d, int r, float s, int64_t M, int RP16,
+                     const Split &sp, float *part, hipStream_t st) {
+  const dim3 grid((unsigned)pr.tiles, (unsigned)sp.S);
+  const GradProblem none{};
+  hipError_t e = hipErrorInvalidValue;
+  switch (RP16 / 16) {
+#define QL_DG(NT)                                                                                            \
+  case NT:                                                                                                   \
+    e = launch(drop_grad_kernel<NT>, grid, 256, st, pr, U, d, r, s, M, sp.chunk, pr.I, part);                \
+    if (e == hipSuccess && sp.S > 1)                                                                         \
+      e = launch(lora_grad_reduce_kernel<NT * 16>, (unsigned)(pr.I / kGradRedRows), 256, st, pr, none, r, s, \
+                 sp.S, pr.I, (const float *)part);                                                           \
+    break;
+    QL_DG(1) QL_DG(2) QL_DG(3) QL_DG(4) QL_DG(5) QL_DG(6) QL_DG(7) QL_DG(8)
+#undef QL_DG
+  }
+  return e;
+}
+
+}  // namespace
+
+size_t linear_drop_workspace(int64_t M, int64_t h, int64_t o, int r) {
+  if (r == 0) return linear_bwd_workspace(M, h, o, r);
+  const size_t f = linear_fwd_workspace(M, h, o, r), b = drop_layout(M, h, o, r).total;
+  return f > b ? f : b;
+}
+
+bool linear_drop_supported(int64_t M, int64_t h, int64_t o, int r) {
+  if (r == 0) return true;
+  const DropLayout L = drop_layout(M, h, o, r);
+  return L.s1.S <= 65535 && L.s2.S <= 65535;
+}
+
+hipError_t launch_linear_fwd_drop(const LinearArgs &a, const DropState &d, const uint16_t *X, const uint16_t *L1,
+                                  const uint16_t *L2, uint16_t *Y, uint16_t *T, void *ws, const Nf4Tables &tab,
+                                  hipStream_t st) {
+  return linear_fwd(a, X, L1, L2, Y, T, ws, tab, st, &d);
+}
+
+hipError_t launch_linear_bwd_drop(const LinearArgs &a, const DropState &d, const uint16_t *X, const uint16_t *T,
+                                  const uint16_t *dY, const uint16_t *L1, const uint16_t *L2, uint16_t *dX,
+                                  float *dL1, float *dL2, void *ws, const Nf4Tables &tab, hipStream_t st) {
+  if (a.r == 0) return launch_linear_bwd(a, X, T, dY, L1, L2, dX, dL1, dL2, ws, tab, st);
+  const DropLayout L = drop_layout(a.M, a.h, a.o, a.r);
+  float *U = at<float>(ws, L.off_u);
+  uint16_t *sU = at<uint16_t>(ws, L.off_su), *L1p = at<uint16_t>(ws, L.off_l1p);
+  RankParams rp{};
+  rp.A = dY; rp.lda = a.o; rp.M = a.M; rp.K = a.o;
+  rp.B = L2; rp.ldb = a.o; rp.r = a.r; rp.s = a.s;
+  rp.ld1 = L.RP16; rp.out2 = sU; rp.ld2 = L.RP64; rp.out32 = U;
+  rp.L1 = L1; rp.h = a.h; rp.ldp = L.RP64; rp.L1p = L1p;
+  hipError_t e = rank_r(rp, false, L.RP16, at<float>(ws, L.off_up), st);
+  if (e != hipSuccess) return e;
+  const GradProblem g1{X, a.h, a.h, nullptr, 0, dL1, false, cdiv(a.h, kGradTile), 0};
+  const GradProblem g2{dY, a.o, a.o, T, a.r, dL2, true, cdiv(a.o, kGradTile), 0};
+  e = drop_grad(g1, U, d, a.r, a.s, a.M, L.RP16, L.s1, at<float>(ws, L.off_g1), st);
+  if (e != hipSuccess) return e;
+  e = lora_grad(GradProblem{}, g2, a.r, a.s, a.M, L.RP16, L.s2, at<float>(ws, L.off_g2), st);
+  if (e != hipSuccess) return e;
+  if (a.M <= 16) {
+    GvdParams vp{};
+    vp.dY = dY; vp.ldy = a.o; vp.M = (int)a.M;
+    vp.codes = a.codes; vp.qabsmax = a.qabsmax; vp.scale2 = a.scale2; vp.mean = a.mean;
+    vp.h = a.h; vp.o = a.o;
+    vp.rows = (int)rup((a.o + L.dxc - 1) / L.dxc, kGvmRows);
+    vp.part = at<float>(ws, L.off_dxp);
+    fill_levels(vp.level, tab);
+    const dim3 grid((unsigned)((a.h + kGvdCols - 1) / kGvdCols), (unsigned)L.dxc);
+    e = launch(nf4_gemv_dx_kernel, grid, kGvmThreads, st, vp);
+    if (e != hipSuccess) return e;
+    const int64_t cg = (a.h / 8 + 63) / 64;
+    return launch(gemv_dx_finish_kernel, (unsigned)(a.M * cg), 256, st, (const float *)vp.part, L.dxc, (int)a.M,
+                  a.h, (const uint16_t *)sU, L.RP64, L1, a.r, dX, a.h, d);
+  }
+  GemmParams gp{};
+  gp.A = dY; gp.lda = a.o;
+  gp.codes = a.codes; gp.qabsmax = a.qabsmax; gp.scale2 = a.scale2; gp.mean = a.mean;
+  gp.ldw = a.h; gp.wrows = a.o;
+  gp.A2 = sU; gp.lda2 = L.RP64; gp.B2 = L1p; gp.ldb2 = L.RP64; gp.b2rows = (int)a.h;
+  gp.ksteps = (int)(a.o / 64);
+  gp.ksteps2 = L.RP64 / 64;
+  gp.M = a.M; gp.N = a.h;
+  gp.C = dX; gp.ldc = a.h;
+  fill_levels(gp.level, tab);
+  gp.drop = d;
+  return launch_nf4_gemm_dx_drop(gp, st);
 }
 
 }  // namespace ql

@@ -41,7 +41,9 @@
 //  matrix read as zero, so the K loop has no branches and no 64-bit address
 //  arithmetic.
 // LoRA: the rank-r term s·(X·L1)·L2 (forward) or s·(dY·L2^T)·L1^T (dX) is added
-//  by extra K steps over (A2, B2) on the same accumulators.
+//  by extra K steps over (A2, B2) on the same accumulators.  With dropout on the
+//  adapter's input (DROP, dX only) those steps run first, and the mask clears the
+//  dropped elements' accumulators before the main loop adds the frozen weight's part.
 
 #include "gemm.h"
 
@@ -88,8 +90,9 @@ constexpr int cmax(int a, int b) { return a > b ? a : b; }
 
 }  // namespace
 
-template <int BM, int BN, bool TRANS>
+template <int BM, int BN, bool TRANS, bool DROP>
 __global__ __launch_bounds__(512) void nf4_gemm_kernel(GemmParams p) {
+  static_assert(TRANS || !DROP, "the mask belongs to the dX direction");
   constexpr int NT = 512, BK = 64;
   constexpr int WTM = BM / 4, WTN = BN / 2, TM = WTM / 32, TN = WTN / 32;
   static_assert(BN == 128 && (BM == 256 || BM == 128), "256 x 128 or 128 x 128 tiles");
@@ -346,6 +349,32 @@ __global__ __launch_bounds__(512) void nf4_gemm_kernel(GemmParams p) {
   // the first LoRA step's operands: the oldest loads, done long before they are used
   LoraStage L0;
   lora_load(0, L0);
+  if constexpr (DROP) {
+    for (int k2 = 0; k2 < p.ksteps2; ++k2) {
+      LoraStage L;
+      if (k2 == 0) L = L0;
+      else lora_load(k2, L);
+      lora_put(L);
+      __syncthreads();
+      mma_step(0, false);
+      __syncthreads();
+    }
+    uint32_t *words = reinterpret_cast<uint32_t *>(sm);
+    keep_tile<BM, BN, NT>(words, p.drop, m0, n0, p.N, tid);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const u32x4 w = *reinterpret_cast<const u32x4 *>(words + ((wn * WTN >> 5) + j) * BM + wm * WTM + 32 * i +
+                                                           8 * q + 4 * g);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] = (w[e] >> l32) & 1u ? acc[i][j][4 * q + e] : 0.0f;
+        }
+    __syncthreads();
+  }
 
   // wait until at most n vector-memory operations of this wave are outstanding
   // (the LDS-bound A loads count; the compiler cannot know that other waves read them)
@@ -404,7 +433,7 @@ __global__ __launch_bounds__(512) void nf4_gemm_kernel(GemmParams p) {
 
   // LoRA K steps (after the main loop, on the same accumulators).  The first one's
   // operands were loaded in the prologue (lora_load above) where registers allow.
-  for (int k2 = 0; k2 < p.ksteps2; ++k2) {
+  for (int k2 = 0; !DROP && k2 < p.ksteps2; ++k2) {
     LoraStage L;
     if (k2 == 0) L = L0;
     else lora_load(k2, L);
@@ -439,11 +468,11 @@ namespace {
 
 inline int64_t cdiv(int64_t x, int64_t m) { return (x + m - 1) / m; }
 
-template <int BM, int BN, bool TRANS>
+template <int BM, int BN, bool TRANS, bool DROP = false>
 hipError_t gemm_launch(GemmParams &gp, hipStream_t st) {
   gp.tiles_m = (int)cdiv(gp.M, BM);
   gp.tiles_n = (int)cdiv(gp.N, BN);
-  return launch(nf4_gemm_kernel<BM, BN, TRANS>, gp.tiles_m * gp.tiles_n, 512, st, gp);
+  return launch(nf4_gemm_kernel<BM, BN, TRANS, DROP>, gp.tiles_m * gp.tiles_n, 512, st, gp);
 }
 
 template <bool TRANS>
@@ -459,6 +488,15 @@ hipError_t gemm_select(GemmParams &gp, hipStream_t st) {
 }
 
 }  // namespace
+
+// the dX direction's choice of tiles, as in gemm_select
+hipError_t launch_nf4_gemm_dx_drop(GemmParams &gp, hipStream_t st) {
+  const int64_t t256 = cdiv(gp.M, 256) * cdiv(gp.N, 256);
+  const int64_t t256x128 = cdiv(gp.M, 256) * cdiv(gp.N, 128);
+  if (gp.M >= 256 && t256 >= 240) return launch_nf4_gemm_wide_dx_drop(gp, st);
+  if (gp.M >= 192 && t256x128 >= 160) return gemm_launch<256, 128, true, true>(gp, st);
+  return gemm_launch<128, 128, true, true>(gp, st);
+}
 
 hipError_t launch_nf4_gemm(GemmParams &gp, bool trans, hipStream_t st) {
   return trans ? gemm_select<true>(gp, st) : gemm_select<false>(gp, st);

@@ -493,6 +493,9 @@ QL_DEV u32x2 wtr4(const uint8_t *ptr) {
 }
 }  // namespace
 
+// DROP: dropout on the adapter's input.  The rank-r steps then run first, and the mask
+// clears the dropped elements' accumulators before the main loop.
+template <bool DROP>
 __global__ __launch_bounds__(kThreads) void nf4_gemm_wide_dx_kernel(GemmParams p) {
   constexpr int kTN = kXTN, kBN = kXBN, kLdc = kXLdc;
   __shared__ __attribute__((aligned(16))) char lds[kXLdsBytes];
@@ -634,6 +637,62 @@ __global__ __launch_bounds__(kThreads) void nf4_gemm_wide_dx_kernel(GemmParams p
     for (int j = 0; j < kTN; ++j)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+
+  // ---- rank-r K steps: A2 = s-scaled U [M][lda2] through ring buffer 0; B2 = L1
+  // padded to [N][ldb2]: lane (n, g) takes row n ^ 1 of its column tile (the
+  // swapped column of the code path), 16 contiguous bytes per MFMA group
+  auto rank_steps = [&]() {
+    if (p.ksteps2 > 0) {
+      const auto rA2 = wrsrc(p.A2 + m0 * p.lda2, mrows * p.lda2 * 2);
+      const auto rB2 = wrsrc(p.B2 + n0 * p.ldb2, nrows * p.ldb2 * 2);
+      uint16_t *a2 = ring;
+      for (int k2 = 0; k2 < p.ksteps2; ++k2) {
+  #pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int ch = tid + kThreads * u, r = ch >> 3, lc = ch & 7;
+          const u32x4 v = wload128(rA2, (int)((r * p.lda2 + lc * 8) * 2), k2 * kBK * 2);
+          *reinterpret_cast<u32x4 *>(a2 + r * kBK + ((lc ^ a_swz(r)) << 3)) = v;
+        }
+        u32x4 b2[kTN][4];
+  #pragma unroll
+        for (int j = 0; j < kTN; ++j)
+  #pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            b2[j][kk] = wload128(rB2, (int)(((64 * wv + 32 * j + (l32 ^ 1)) * p.ldb2 + 32 * g + 8 * kk) * 2),
+                                 k2 * kBK * 2);
+        __syncthreads();
+  #pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          u32x4 a[kTM];
+          read_a(0, kk, a);
+  #pragma unroll
+          for (int i = 0; i < kTM; ++i)
+  #pragma unroll
+            for (int j = 0; j < kTN; ++j) acc[i][j] = wmfma(a[i], b2[j][kk], acc[i][j]);
+        }
+        __syncthreads();
+      }
+    }
+  };
+  if constexpr (DROP) {
+    __syncthreads();  // pair table written (the ring's space follows it)
+    rank_steps();
+    uint32_t *words = reinterpret_cast<uint32_t *>(ring);
+    keep_tile<kBM, kXBN, kThreads>(words, p.drop, m0, n0, p.N, tid);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kTM; ++i)
+#pragma unroll
+      for (int j = 0; j < kTN; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const u32x4 w = *reinterpret_cast<const u32x4 *>(words + (2 * wv + j) * kBM + 32 * i + 8 * q + 4 * g);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            acc[i][j][4 * q + e] = (w[e] >> (l32 ^ 1)) & 1u ? acc[i][j][4 * q + e] : 0.0f;
+        }
+    // (the barrier below orders these reads before the first copies into the ring)
+  }
 
   const int nk = p.ksteps;
   // stage s lives in slot s % 2 of the A ring, slot s % 3 of the code and a_hat
@@ -787,40 +846,7 @@ __global__ __launch_bounds__(kThreads) void nf4_gemm_wide_dx_kernel(GemmParams p
   __builtin_amdgcn_s_waitcnt(0);  // no copy of a stage past the end may still land in LDS
   __syncthreads();
 
-  // ---- rank-r K steps: A2 = s-scaled U [M][lda2] through ring buffer 0; B2 = L1
-  // padded to [N][ldb2]: lane (n, g) takes row n ^ 1 of its column tile (the
-  // swapped column of the code path), 16 contiguous bytes per MFMA group
-  if (p.ksteps2 > 0) {
-    const auto rA2 = wrsrc(p.A2 + m0 * p.lda2, mrows * p.lda2 * 2);
-    const auto rB2 = wrsrc(p.B2 + n0 * p.ldb2, nrows * p.ldb2 * 2);
-    uint16_t *a2 = ring;
-    for (int k2 = 0; k2 < p.ksteps2; ++k2) {
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int ch = tid + kThreads * u, r = ch >> 3, lc = ch & 7;
-        const u32x4 v = wload128(rA2, (int)((r * p.lda2 + lc * 8) * 2), k2 * kBK * 2);
-        *reinterpret_cast<u32x4 *>(a2 + r * kBK + ((lc ^ a_swz(r)) << 3)) = v;
-      }
-      u32x4 b2[kTN][4];
-#pragma unroll
-      for (int j = 0; j < kTN; ++j)
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          b2[j][kk] = wload128(rB2, (int)(((64 * wv + 32 * j + (l32 ^ 1)) * p.ldb2 + 32 * g + 8 * kk) * 2),
-                               k2 * kBK * 2);
-      __syncthreads();
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        u32x4 a[kTM];
-        read_a(0, kk, a);
-#pragma unroll
-        for (int i = 0; i < kTM; ++i)
-#pragma unroll
-          for (int j = 0; j < kTN; ++j) acc[i][j] = wmfma(a[i], b2[j][kk], acc[i][j]);
-      }
-      __syncthreads();
-    }
-  }
+  if constexpr (!DROP) rank_steps();
 
   // ---- epilogue: fp32 -> bf16 through LDS (accumulator column l32 is output column
   // l32 ^ 1 of its tile), then coalesced 16-byte stores
@@ -851,9 +877,15 @@ hipError_t launch_nf4_gemm_wide(GemmParams &gp, bool trans, int bn, hipStream_t 
   const unsigned grid = (unsigned)(gp.tiles_m * gp.tiles_n);
   // the dX kernel has 256-wide tiles only: a 128-wide version measured slower than
   // the eight-wave kernel on a 4096 x 4096 weight with 2048 tokens (101 vs 90 us)
-  if (trans) return bn == 256 ? launch(nf4_gemm_wide_dx_kernel, grid, kThreads, st, gp) : hipErrorInvalidValue;
+  if (trans) return bn == 256 ? launch(nf4_gemm_wide_dx_kernel<false>, grid, kThreads, st, gp) : hipErrorInvalidValue;
   return bn == 256 ? launch(nf4_gemm_wide_fwd_kernel<2>, grid, kThreads, st, gp)
                    : launch(nf4_gemm_wide_fwd_kernel<1>, grid, kThreads, st, gp);
+}
+
+hipError_t launch_nf4_gemm_wide_dx_drop(GemmParams &gp, hipStream_t st) {
+  gp.tiles_m = (int)((gp.M + kBM - 1) / kBM);
+  gp.tiles_n = (int)((gp.N + kXBN - 1) / kXBN);
+  return launch(nf4_gemm_wide_dx_kernel<true>, (unsigned)(gp.tiles_m * gp.tiles_n), kThreads, st, gp);
 }
 
 }  // namespace ql

@@ -71,7 +71,8 @@ typedef enum {
   QLORA_OP_LINEAR_BWD = 2,   /* a = M tokens, b = h, c = o */
   QLORA_OP_NORM_BWD = 3,     /* a = M rows, b = h */
   QLORA_OP_LOSS_FWD = 4,     /* a = M tokens, b = h, c = V */
-  QLORA_OP_LOSS_BWD = 5      /* a = M tokens, b = h, c = V */
+  QLORA_OP_LOSS_BWD = 5,     /* a = M tokens, b = h, c = V */
+  QLORA_OP_LINEAR_DROPOUT = 6 /* a = M tokens, b = h, c = o: either direction */
 } qlora_op_t;
 
 #define QLORA_BLOCK 64      /* weights per first-level scale ([MC] "2. Double quantization") */
@@ -238,6 +239,46 @@ qlora_status_t qlora_linear_bwd_cb(const qlora_nf4_weight_t *W, qlora_codebook_t
                                    const uint16_t *T, const uint16_t *dY, int64_t M, const uint16_t *L1,
                                    const uint16_t *L2, int32_t r, float s, uint16_t *dX, float *dL1, float *dL2,
                                    void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Dropout from a counter-based generator, with a mask that is never stored (the pages'
+ * adapter configuration, [TT] "LoraConfig", sets lora_dropout = 0.05 beside r and alpha).
+ * Element e of a tensor has 16 random bits: the (e % 8)-th 16-bit piece, low half of a
+ * word first, of Philox4x32-7 (Salmon et al., 2011) with key `seed` and the 128-bit
+ * counter (offset + e / 8, 0).  It is kept when its bits reach t = rint(65536 p); kept
+ * values are scaled by 65536 / (65536 - t), which is unbiased at the probability t / 65536
+ * that 16 bits express.  A dropped element is 0 whatever it held.
+ *  p    0 <= p < 1 with t <= 65535.
+ *  rng  DEVICE pointer to two uint64: {seed, offset}, 8-byte aligned, read when the call
+ *       runs: a captured graph advances the offset between replays by writing there.
+ *       A forward and its backward take the same state; the next use of n elements takes
+ *       an offset at least ceil(n / 8) further.
+ *
+ * qlora_dropout  out[e] = dropout of x[e], n elements of float32 or bf16 (one rounding).
+ *  The same call on a gradient is the backward.  out may be x.  16-byte aligned.
+ *
+ * qlora_linear_fwd_dropout / qlora_linear_bwd_dropout — the linear layer with dropout on
+ * its adapter's input: element (m, k) of X is element m*h + k.  With s' = s / (1 - t/65536)
+ * and keep the 0/1 mask:
+ *   T = (keep ⊙ X)·L1                 Y  = X·W_hat + s'·T·L2
+ *   U = dY·L2^T                       dX = dY·W_hat^T + s'·keep ⊙ (U·L1^T)
+ *   dL1 = s'·(keep ⊙ X)^T·U           dL2 = s'·T^T·dY
+ *  T (bf16, without the scale) is the forward's output for the backward.  dL1 keeps U to
+ *  float32's 24 bits.  The frozen part sees all of X.  Other arguments, layouts and errors
+ *  as qlora_linear_fwd_cb and qlora_linear_bwd_cb; r = 0 is the plain linear.
+ *  workspace: qlora_workspace_size(QLORA_OP_LINEAR_DROPOUT, M, h, o, r) bytes.
+ */
+qlora_status_t qlora_dropout(const void *x, qlora_dtype_t dtype, int64_t n, double p, const uint64_t *rng, void *out,
+                             void *stream);
+qlora_status_t qlora_linear_fwd_dropout(const qlora_nf4_weight_t *W, qlora_codebook_t codebook, const uint16_t *X,
+                                        int64_t M, const uint16_t *L1, const uint16_t *L2, int32_t r, float s,
+                                        double p, const uint64_t *rng, uint16_t *Y, uint16_t *T, void *workspace,
+                                        size_t ws_bytes, void *stream);
+qlora_status_t qlora_linear_bwd_dropout(const qlora_nf4_weight_t *W, qlora_codebook_t codebook, const uint16_t *X,
+                                        const uint16_t *T, const uint16_t *dY, int64_t M, const uint16_t *L1,
+                                        const uint16_t *L2, int32_t r, float s, double p, const uint64_t *rng,
+                                        uint16_t *dX, float *dL1, float *dL2, void *workspace, size_t ws_bytes,
+                                        void *stream);
 
 /*
  * qlora_merge_adapter — merge a trained adapter into the frozen base

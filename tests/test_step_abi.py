@@ -86,3 +86,55 @@ def test_loss_own_refusals():
     # the backward's workspace follows a piece of the vocabulary, not the whole of it
     small, large = (nf4.workspace_size(nf4.QLORA_OP_LOSS_BWD, 65536, 64, V) for V in (8192, 131072))
     assert large == small
+
+
+def drop(x=A[0], dt=1, n=10, p=0.1, rng=A[1], out=A[2]):
+    return lib.qlora_dropout(x, dt, n, p, rng, out, None)
+
+
+BAD_DROP = [dict(p=-0.1), dict(p=1.0), dict(p=NAN), dict(p=0.999999), dict(rng=None), dict(rng=ctypes.c_void_p(0x100004))]
+
+
+@pytest.mark.parametrize("bad", BAD_DROP + [dict(x=None), dict(out=None), dict(dt=2), dict(n=0), dict(x=ODD), dict(out=ODD)])
+def test_dropout_refusals(bad):
+    assert drop(**bad) == INV
+    assert drop(n=(1 << 40) + 1) == UNS
+
+
+def weight(h=128, o=64, codes=A[20]):
+    return nf4.NF4WeightT(codes.value if codes else None, A[21].value, A[22].value, A[23].value, h, o)
+
+
+def lin_fwd(W=None, cb=0, X=A[0], M=4, L1=A[1], L2=A[2], r=8, p=0.1, rng=A[3], Y=A[4], T=A[5], ws=A[6], wb=1 << 40):
+    return lib.qlora_linear_fwd_dropout(ctypes.byref(W or weight()), cb, X, M, L1, L2, r, 1.0, p, rng, Y, T, ws, wb, None)
+
+
+def lin_bwd(W=None, cb=0, X=A[0], T=A[5], dY=A[7], M=4, L1=A[1], L2=A[2], r=8, p=0.1, rng=A[3], dX=A[8], dL1=A[9],
+            dL2=A[10], ws=A[6], wb=1 << 40):
+    return lib.qlora_linear_bwd_dropout(ctypes.byref(W or weight()), cb, X, T, dY, M, L1, L2, r, 1.0, p, rng, dX, dL1,
+                                        dL2, ws, wb, None)
+
+
+@pytest.mark.parametrize("call", [lin_fwd, lin_bwd])
+@pytest.mark.parametrize("bad", BAD_DROP + [
+    dict(cb=3), dict(X=None), dict(X=ODD), dict(M=0), dict(M=(1 << 31) + 1), dict(L1=None), dict(L2=None), dict(r=-1),
+    dict(r=129), dict(T=None), dict(T=ODD), dict(ws=None), dict(wb=64), dict(ws=ctypes.c_void_p(0x100010)),
+    dict(W=weight(h=100)), dict(W=weight(o=32)), dict(W=weight(codes=None)), dict(W=weight(codes=ODD)),
+])
+def test_linear_dropout_refusals(call, bad):
+    assert call(**bad) == INV
+
+
+def test_linear_dropout_own_refusals():
+    assert lin_fwd(Y=None) == INV
+    for k in ("dY", "dX", "dL1", "dL2"):
+        assert lin_bwd(**{k: None}) == INV and lin_bwd(**{k: ODD}) == INV
+    assert lin_fwd(r=0, Y=None) == INV and lin_bwd(r=0, dY=None) == INV     # the plain linear's own checks
+    op = nf4.QLORA_OP_LINEAR_DROPOUT
+    for M, h, o, r in ((1, 64, 64, 1), (16, 1024, 1024, 64), (2048, 8192, 22016, 64)):
+        assert nf4.workspace_size(op, M, h, o, r) >= nf4.workspace_size(nf4.QLORA_OP_LINEAR_FWD, M, h, o, r)
+    assert nf4.workspace_size(op, 17, 64, 64, 0) == 0
+    with pytest.raises(nf4.QloraError):
+        nf4.workspace_size(op, 0, 64, 64, 8)
+    big = weight(h=1 << 20, o=64)
+    assert lin_bwd(W=big, M=1 << 31, wb=(1 << 62)) == UNS                   # too many token splits
