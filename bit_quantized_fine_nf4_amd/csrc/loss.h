@@ -34,8 +34,9 @@ struct LogitParams {
   f32x2 *part;          // [tiles_v][ldp]
   int64_t ldp;
   float *zlab;          // [n] the label's logit
-  // gradient: G = (exp(z - lse) - onehot) * dloss
+  // gradient: G = (exp(z - lse) - onehot) * (dloss / top)
   const float *lse, *dloss;  // [n]
+  const float *top;          // the largest |dloss| (device)
   uint16_t *G;          // [n][ldg] bf16, ldg = tiles_v * 256; zero past nvoc
   int64_t ldg;
 };
@@ -50,6 +51,7 @@ struct HeadGradParams {
   const uint16_t *W;   // dH: [nvoc][h] rows of this piece
   const uint16_t *H;   // dW: [n][h] compact hidden states
   const int *count;
+  const float *top;    // dW: G's common factor
   int64_t h, nvoc;
   int tiles_m, tiles_n;
   int64_t kper;        // dH: vocabulary entries per split (a multiple of 64)

@@ -7,7 +7,11 @@
 // vocabulary, each token's maximum and sum of exponentials; the backward computes z
 // again, piece by piece of the vocabulary, turns each piece into G in bf16 and multiplies
 // it at once.  G is rounded to bf16 because it is a matrix-core operand of the two
-// gradient products; their sums are float32.
+// gradient products; their sums are float32.  What is rounded is G without the largest
+// |dloss|, which multiplies the sums instead: with the mean's one dloss for all tokens a
+// label's entry is then -1 (+ its probability) and rounds to almost nothing, where
+// -1 / count would be off by up to 2^-9 in every token alike (dH's error against 64 bits
+// 2.6e-3 of its norm, now that of its own rounding, 1.7e-3).
 //
 // Tokens whose label is outside [0, V) (prompt and padding tokens) carry no loss.  The
 // others are first gathered into a compact copy of H, so such tokens cost no products
@@ -31,16 +35,18 @@ constexpr int kSelThreads = 1024;
 }  // namespace
 
 // The tokens with a label in [0, V), in order: idx[i], label[i], and with `lse` the
-// compact lse and dloss.  Tokens without one get loss = lse = 0 (forward).
+// compact lse and dloss and the largest |dloss|.  Tokens without one get loss = lse = 0 (forward).
 __global__ __launch_bounds__(kSelThreads) void loss_select_kernel(const int64_t *labels, int64_t M, int64_t V,
                                                                   int *count, int *idx, int *label,
                                                                   const float *lse, const float *dloss,
-                                                                  float *c_lse, float *c_dloss, float *out_loss,
-                                                                  float *out_lse) {
+                                                                  float *c_lse, float *c_dloss, float *c_top,
+                                                                  float *out_loss, float *out_lse) {
   __shared__ int sums[2][kSelThreads / 64];
+  __shared__ float tops[kSelThreads / 64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int base = 0;
   int buf = 0;
+  float top = 0.0f;
   for (int64_t m0 = 0; m0 < M; m0 += 4 * kSelThreads, buf ^= 1) {
     int64_t lab[4];
     int ok[4], mine = 0;
@@ -76,6 +82,7 @@ __global__ __launch_bounds__(kSelThreads) void loss_select_kernel(const int64_t 
         if (lse) {
           c_lse[at] = lse[m];
           c_dloss[at] = dloss[m];
+          top = fmaxf(top, fabsf(dloss[m]));
         }
         ++at;
       } else if (out_loss && m < M) {
@@ -86,6 +93,16 @@ __global__ __launch_bounds__(kSelThreads) void loss_select_kernel(const int64_t 
     base += all;
   }
   if (tid == 0) *count = base;
+  if (!lse) return;  // the whole workgroup
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+  if (lane == 0) tops[wave] = top;
+  __syncthreads();
+  if (tid == 0) {
+#pragma unroll
+    for (int w = 1; w < kSelThreads / 64; ++w) top = fmaxf(top, tops[w]);
+    *c_top = top;
+  }
 }
 
 // Row i of the compact copy = row idx[i] of H (i < n); with dH, the rows without a label
@@ -134,9 +151,11 @@ __global__ __launch_bounds__(256) void loss_finish_kernel(const f32x2 *part, int
   }
 }
 
-// dH[idx[i]] = bf16(sum over the splits of part[split][i]), eight values per thread.
+// dH[idx[i]] = bf16(top * sum over the splits of part[split][i]), eight values per thread.
 __global__ __launch_bounds__(256) void loss_dh_kernel(const float *part, int splits, int64_t rows, int64_t h,
-                                                      const int *count, const int *idx, uint16_t *dH) {
+                                                      const int *count, const int *idx, const float *c_top,
+                                                      uint16_t *dH) {
+  const float top = *c_top;
   const int64_t per = h / 8, total = (int64_t)*count * per;
   for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
     const int64_t i = e / per, c = e % per * 8;
@@ -147,6 +166,8 @@ __global__ __launch_bounds__(256) void loss_dh_kernel(const float *part, int spl
       a += *reinterpret_cast<const f32x4 *>(q);
       b += *reinterpret_cast<const f32x4 *>(q + 4);
     }
+    a *= top;
+    b *= top;
     *reinterpret_cast<u32x4 *>(dH + (int64_t)idx[i] * h + c) =
         u32x4{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3])};
   }
@@ -177,7 +198,7 @@ int loss_splits(int64_t M, int64_t h, int64_t piece) {
 }
 
 struct LossLayout {
-  size_t count, idx, label, lse, dloss, hc, stat, zlab, g, part, total;
+  size_t count, top, idx, label, lse, dloss, hc, stat, zlab, g, part, total;
   int64_t piece, kper;
   int splits;
 };
@@ -187,6 +208,7 @@ LossLayout loss_layout(int64_t M, int64_t h, int64_t V, bool bwd) {
   size_t off = 0;
   auto take = [&](size_t bytes) { const size_t at = off; off += (bytes + 255) / 256 * 256; return at; };
   L.count = take(4);
+  L.top = take(4);
   L.idx = take((size_t)M * 4);
   L.label = take((size_t)M * 4);
   L.hc = take((size_t)M * h * 2);
@@ -228,7 +250,8 @@ hipError_t launch_loss_fwd(const LossArgs &a, float *loss, float *lse, void *ws,
   int *count = at<int>(ws, L.count), *idx = at<int>(ws, L.idx), *label = at<int>(ws, L.label);
   uint16_t *Hc = at<uint16_t>(ws, L.hc);
   hipError_t e = launch(loss_select_kernel, 1, kSelThreads, st, a.labels, a.M, a.V, count, idx, label,
-                        (const float *)nullptr, (const float *)nullptr, (float *)nullptr, (float *)nullptr, loss, lse);
+                        (const float *)nullptr, (const float *)nullptr, (float *)nullptr, (float *)nullptr,
+                        (float *)nullptr, loss, lse);
   if (e != hipSuccess) return e;
   e = launch(loss_gather_kernel, grid4(a.M), 256, st, a.H, a.M, a.h, (const int *)count, (const int *)idx, Hc, a.labels,
              a.V, (uint16_t *)nullptr);
@@ -247,9 +270,9 @@ hipError_t launch_loss_bwd(const LossArgs &a, const float *lse, const float *dlo
   const LossLayout L = loss_layout(a.M, a.h, a.V, true);
   int *count = at<int>(ws, L.count), *idx = at<int>(ws, L.idx), *label = at<int>(ws, L.label);
   uint16_t *Hc = at<uint16_t>(ws, L.hc);
-  float *c_lse = at<float>(ws, L.lse), *c_dl = at<float>(ws, L.dloss);
+  float *c_lse = at<float>(ws, L.lse), *c_dl = at<float>(ws, L.dloss), *top = at<float>(ws, L.top);
   hipError_t e = launch(loss_select_kernel, 1, kSelThreads, st, a.labels, a.M, a.V, count, idx, label, lse, dloss,
-                        c_lse, c_dl, (float *)nullptr, (float *)nullptr);
+                        c_lse, c_dl, top, (float *)nullptr, (float *)nullptr);
   if (e != hipSuccess) return e;
   e = launch(loss_gather_kernel, grid4(a.M), 256, st, a.H, a.M, a.h, (const int *)count, (const int *)idx, Hc, a.labels,
              a.V, dH);
@@ -259,11 +282,11 @@ hipError_t launch_loss_bwd(const LossArgs &a, const float *lse, const float *dlo
     const int64_t nvoc = a.V - v0 < L.piece ? a.V - v0 : L.piece;
     LogitParams p{};
     p.W = a.W + v0 * a.h, p.H = Hc, p.count = count, p.label = label, p.h = a.h, p.v0 = v0, p.nvoc = nvoc;
-    p.lse = c_lse, p.dloss = c_dl, p.G = at<uint16_t>(ws, L.g), p.ldg = L.piece;
+    p.lse = c_lse, p.dloss = c_dl, p.top = top, p.G = at<uint16_t>(ws, L.g), p.ldg = L.piece;
     e = launch_logit_grad(p, a.M, st);
     if (e != hipSuccess) return e;
     HeadGradParams q{};
-    q.G = p.G, q.ldg = L.piece, q.W = p.W, q.H = Hc, q.count = count, q.h = a.h, q.nvoc = nvoc;
+    q.G = p.G, q.ldg = L.piece, q.W = p.W, q.H = Hc, q.count = count, q.top = top, q.h = a.h, q.nvoc = nvoc;
     q.kper = L.kper, q.part = part, q.rows = a.M, q.add = v0 > 0;
     // the last piece may fill fewer splits: the others' sums are whole already
     e = launch_head_dh(q, (int)cdiv(nvoc, L.kper), a.M, st);
@@ -276,7 +299,7 @@ hipError_t launch_loss_bwd(const LossArgs &a, const float *lse, const float *dlo
   }
   const int64_t groups = cdiv(a.M * (a.h / 8), 256);
   return launch(loss_dh_kernel, (unsigned)(groups < 8192 ? groups : 8192), 256, st, (const float *)part, L.splits, a.M,
-                a.h, (const int *)count, (const int *)idx, dH);
+                a.h, (const int *)count, (const int *)idx, (const float *)top, dH);
 }
 
 }  // namespace ql

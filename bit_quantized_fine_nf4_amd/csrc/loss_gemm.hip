@@ -239,7 +239,7 @@ QL_DEV int acc_row(int v, int g) { return 8 * (v >> 2) + 4 * g + (v & 3); }
 // its softmax statistics need one exchange between lanes.
 // GRAD false: part[tile][token] = (max, sum of exp(z - max)) over the tile's rows, and
 // zlab of the tokens whose label is among them.
-// GRAD true: G[token][v] = bf16((exp(z - lse) - [v is the label]) * dloss).
+// GRAD true: G[token][v] = bf16((exp(z - lse) - [v is the label]) * (dloss / top)).
 template <int BV, int BT, int WV, int S, bool GRAD>
 __global__ __launch_bounds__(kThreads) void head_logits_kernel(LogitParams p) {
   constexpr int WT = 4 / WV, TA = BV / WV / 32, TB = BT / WT / 32;
@@ -308,12 +308,13 @@ __global__ __launch_bounds__(kThreads) void head_logits_kernel(LogitParams p) {
     }
   } else {
     uint16_t *cs = reinterpret_cast<uint16_t *>(lds);
+    const float top = *p.top;
 #pragma unroll
     for (int j = 0; j < TB; ++j) {
       const int col = wb + 32 * j + l32;
       const int64_t t = t0 + col;
       const bool live = t < n;
-      const float lse = live ? p.lse[t] : 0.0f, dl = live ? p.dloss[t] : 0.0f;
+      const float lse = live ? p.lse[t] : 0.0f, dl = live && top > 0.0f ? p.dloss[t] / top : 0.0f;
       const int64_t lab = live ? (int64_t)p.label[t] - p.v0 - v0 : -1;
 #pragma unroll
       for (int i = 0; i < TA; ++i)
@@ -380,7 +381,7 @@ __global__ __launch_bounds__(kThreads) void head_dh_kernel(HeadGradParams p) {
       }
 }
 
-// dW[v][k] = bf16(sum over the tokens of G[token][v] H[token][k]).
+// dW[v][k] = bf16(top * sum over the tokens of G[token][v] H[token][k]).
 template <int S>
 __global__ __launch_bounds__(kThreads) void head_dw_kernel(HeadGradParams p) {
   constexpr int BM = 256, BN = 256, TA = 4, TB = 4, kLdc = BN + 8;
@@ -402,6 +403,7 @@ __global__ __launch_bounds__(kThreads) void head_dw_kernel(HeadGradParams p) {
   clear(acc);
   product<S, TA, TB>(A, B, ring, (n + kBK - 1) / kBK, lane, wv, acc);
   uint16_t *cs = reinterpret_cast<uint16_t *>(lds);
+  const float top = n > 0 ? *p.top : 0.0f;
 #pragma unroll
   for (int i = 0; i < TA; ++i)
 #pragma unroll
@@ -409,7 +411,7 @@ __global__ __launch_bounds__(kThreads) void head_dw_kernel(HeadGradParams p) {
 #pragma unroll
       for (int v = 0; v < 16; ++v)
         cs[(wa + 32 * i + acc_row(v, g)) * kLdc + wb + 32 * j + l32] =
-            (uint16_t)(pack_bf16x2(acc[i][j][v], 0.0f) & 0xFFFFu);
+            (uint16_t)(pack_bf16x2(top * acc[i][j][v], 0.0f) & 0xFFFFu);
   __syncthreads();
   for (int ch = threadIdx.x; ch < BM * BN / 8; ch += kThreads) {
     const int row = ch / (BN / 8), c8 = ch % (BN / 8);
