@@ -4,21 +4,21 @@
 //   dH      = G · W               (split over the vocabulary, float32 partial sums)
 //   dW      = G^T · H
 // One main loop serves all three.  Four waves (one per SIMD) share a tile through LDS;
-// each computes TA x TB MFMA tiles of 32 x 32 (v_mfma_f32_32x32x16_bf16), 64 deep per
-// step.  Both operands go from memory straight into LDS (buffer_load ... lds, 16 bytes
+// each computes TA x TB MFMA tiles of 32 x 32 (v_mfma_f32_32x32x16_bf16), BK deep per
+// stage.  Both operands go from memory straight into LDS (buffer_load ... lds, 16 bytes
 // per lane) in a ring of stages.  An operand is stored in one of two ways:
-//   rows   k runs along memory: a stage is [rows][64 k] in 128-byte rows whose 16-byte
-//          chunks are XOR-swizzled by row; a fragment (8 consecutive k of one row) is
+//   rows   k runs along memory: a stage is [rows][BK] with 16-byte chunks XOR-swizzled
+//          by row; a fragment (8 consecutive k of one row) is
 //          one 16-byte read;
-//   cols   the tile's own index runs along memory: a stage is [64 k][cols] as it is,
+//   cols   the tile's own index runs along memory: a stage is [BK][cols] as it is,
 //          whose 64-byte units are XOR-swizzled by k % 4; a fragment is two transposing
 //          reads (ds_read_b64_tr_b16), whose 32-lane phases name 4 rows k of one unit
 //          and so cover the 64 banks once.
-// Within a step lane group g = lane / 32 owns k in [32 g, 32 g + 32) and MFMA group kk
-// takes k = 32 g + 8 kk + 0..7 for both operands.  The fragments of group kk + 1 are
-// read while group kk's MFMAs run.  One barrier per step, after the third group: by then
-// the step's last fragments are read, so its slot takes the copy S stages ahead, and the
-// fourth group's MFMAs cover those copies and the next step's first reads.
+// MFMA group kk of a stage takes k = 16 kk + 8 (lane / 32) + 0..7 of both operands.  The
+// fragments of group kk + 1 are read while group kk's MFMAs run.  One barrier per stage,
+// before its last group: by then the stage's last fragments are read, so its slot takes
+// the copy S stages ahead, and the last group's MFMAs cover those copies' issue and the
+// next stage's first reads.
 // Rows past an operand's end read as zero (buffer bounds).
 
 #include "loss.h"
@@ -32,19 +32,31 @@ namespace {
 
 typedef short ls16x4 __attribute__((ext_vector_type(4)));
 
-QL_DEV __amdgpu_buffer_rsrc_t lrsrc(const void *base, int64_t bytes) {
+// Buffer descriptor over [base, base + bytes), for loads whose rows past the end read zero.
+QL_DEV u32x4 lrsrc(const void *base, int64_t bytes) {
   const int64_t cap = 0x7FFFFFF0;
-  const int32_t n = (int32_t)(bytes < 0 ? 0 : (bytes > cap ? cap : bytes));
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, n, 0x00020000);
+  const uint32_t n = (uint32_t)(bytes < 0 ? 0 : (bytes > cap ? cap : bytes));
+  const uint64_t at = reinterpret_cast<uint64_t>(base);
+  return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)at),
+               (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)(at >> 32) & 0xFFFFu)),
+               (uint32_t)__builtin_amdgcn_readfirstlane((int)n), 0x00020000u};
 }
 QL_DEV f32x16 lmfma(u32x4 a, u32x4 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
                                                 0, 0);
 }
-// (device functions, not builtins inline in a kernel template's lambda, where the host
-// pass of this compiler drops the kernel's launch stub)
-QL_DEV void lload_lds(__amdgpu_buffer_rsrc_t r, uint16_t *dst, int voff, int soff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)dst, 16, voff, soff, 0, 0);
+// 16 bytes per lane from a buffer straight into LDS: lane L's bytes land at LDS address
+// at + 16 L; at and soff are the wave's.  It has no register result, so nothing of the compiler's is in
+// flight with it; its completion is awaited by the kernel's own vmcnt waits.  It is written
+// in assembly because the compiler, which knows of the builtin that some LDS is being
+// written, waits for every outstanding copy before each transposing LDS read: with it the
+// dH and dW products of 4096 tokens x 8192 x 32000 took 2.4 and 2.2 ms.  (m0 is a reserved
+// register that the compiler writes right before each use of its own; these kernels have
+// none.)
+QL_DEV void lload_lds(u32x4 rsrc, int at, int voff, int soff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "s"(at), "v"(voff), "s"(rsrc), "s"(soff));
 }
 QL_DEV u32x4 ltr_pair(const uint16_t *lo, const uint16_t *hi) {
   typedef __attribute__((address_space(3))) ls16x4 lds_s16x4;
@@ -62,55 +74,63 @@ QL_DEV void lbarrier() {
 }
 
 constexpr int kThreads = 256;
-constexpr int kBK = 64;
+constexpr int kWaves = 4;
 
-// An operand stored in rows: R rows of the tile, k along memory.  `base`: the tile's
-// first row, `bytes`: from there to the operand's end.
-template <int R>
+// An operand stored in rows: R rows of the tile, k along memory, BK of it per stage.
+// `base`: the tile's first row, `bytes`: from there to the operand's end.  Row r's 16-byte
+// chunks sit at chunk ^ f(r), so that the 16 lanes of a read phase (one chunk of 16
+// consecutive rows) cover the 64 banks once.
+template <int R, int BK>
 struct RowOperand {
-  static constexpr int kElems = R * kBK;
-  static constexpr int kCopies = R / 32;  // 1 KB copies (8 rows) per wave and stage
-  static_assert(kCopies == 1 || kCopies % 2 == 0, "the swizzle of a copy depends on its parity");
-  __amdgpu_buffer_rsrc_t rsrc;
+  static constexpr int kElems = R * BK;
+  static constexpr int CH = BK / 8;               // chunks per row
+  static constexpr int kRows = 64 / CH;           // rows per 1 KB copy
+  static constexpr int kBlocks = R / kRows;       // copies per stage
+  static constexpr int kCopies = kBlocks < kWaves ? 1 : kBlocks / kWaves;  // per wave
+  static_assert(kCopies == 1 || kCopies % 2 == 0, "a copy's swizzle depends on its parity");
+  u32x4 rsrc;
   int voff[2], step;
-  int frag;  // element offset of the lane's row in a stage
-  int swz;
+  int frag, swz;
+  static QL_DEV int f(int r) { return (r / (16 / CH)) & (CH - 1); }
+  // with fewer copies than waves two waves make the same one: every wave's count of
+  // outstanding copies stays the same
+  static QL_DEV int block(int wv, int c) { return kBlocks < kWaves ? wv % kBlocks : wv * kCopies + c; }
   QL_DEV void init(const uint16_t *base, int64_t ld, int64_t bytes, int lane, int wv, int first_row) {
     rsrc = lrsrc(base, bytes);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      const int r = 8 * (wv * kCopies + c) + (lane >> 3), lc = (lane & 7) ^ ((r >> 1) & 7);
+      const int r = kRows * block(wv, c) + lane / CH, lc = (lane % CH) ^ f(r);
       voff[c] = (int)((r * ld + lc * 8) * 2);
     }
-    step = __builtin_amdgcn_readfirstlane((int)(8 * ld * 2));
-    const int r = first_row + (lane & 31);  // the tile rows are multiples of 32, so row % 16 is the lane's
-    frag = r * kBK;
-    swz = (r >> 1) & 7;
+    step = __builtin_amdgcn_readfirstlane((int)(kRows * ld * 2));
+    const int r = first_row + (lane & 31);  // MFMA tiles are 32 rows apart: f is the same in all of them
+    frag = r * BK;
+    swz = f(r);
   }
-  QL_DEV void copy(uint16_t *stage, int wv, int kt_) const {
+  // copy c of stage kt into the slot at LDS address `at`
+  QL_DEV void copy(int at, int wv, int kt_, int c) const {
     const int kt = __builtin_amdgcn_readfirstlane(kt_);
-#pragma unroll
-    for (int c = 0; c < kCopies; ++c)
-      lload_lds(rsrc, stage + (wv * kCopies + c) * 512, voff[c & 1], kt * kBK * 2 + (c & ~1) * step);
+    lload_lds(rsrc, at + block(wv, c) * 1024, voff[c & 1], kt * BK * 2 + (c & ~1) * step);
   }
   QL_DEV u32x4 read(const uint16_t *stage, int lane, int t, int kk) const {
-    return *reinterpret_cast<const u32x4 *>(stage + frag + t * 32 * kBK + (((4 * (lane >> 5) + kk) ^ swz) << 3));
+    return *reinterpret_cast<const u32x4 *>(stage + frag + t * 32 * BK + (((2 * kk + (lane >> 5)) ^ swz) << 3));
   }
 };
 
-// An operand stored in columns: C columns of the tile along memory, k down the rows.
-template <int C>
+// An operand stored in columns: C columns of the tile along memory, k down the rows.  A
+// row's 64-byte units sit at unit ^ (k % 4).
+template <int C, int BK>
 struct ColOperand {
-  static constexpr int kElems = C * kBK;
-  static constexpr int kCopies = C / 32;
+  static constexpr int kElems = C * BK;
+  static constexpr int kCopies = C * BK / 512 / kWaves;
   static constexpr int kPerCopy = 512 / C;        // rows k per 1 KB copy
   static constexpr int kLanes = 64 / kPerCopy;    // lanes (16-byte chunks) per row
-  const uint16_t *base;
-  int64_t ld, bytes;
-  int voff[2], step;
-  int frag, frag2;  // element offsets of the lane's unit for tiles of even and odd index
-  QL_DEV void init(const uint16_t *b, int64_t l, int64_t n, int lane, int wv, int first_col) {
-    base = b, ld = l, bytes = n;
+  u32x4 rsrc;
+  int voff[2], step, stride;
+  int frag, unit;
+  // rows [0, k) of `base` are within 2^31 bytes (kernels walk longer sums in segments)
+  QL_DEV void init(const uint16_t *base, int64_t ld, int64_t bytes, int lane, int wv, int first_col) {
+    rsrc = lrsrc(base, bytes);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int k = kPerCopy * (wv * kCopies + c) + lane / kLanes, pc = lane % kLanes;
@@ -118,45 +138,46 @@ struct ColOperand {
       voff[c] = (int)((k * ld + lc * 8) * 2);
     }
     step = __builtin_amdgcn_readfirstlane((int)(kPerCopy * ld * 2));
+    stride = __builtin_amdgcn_readfirstlane((int)(BK * ld * 2));
     const int c = lane & 15, half = (lane >> 4) & 1, g = lane >> 5;
-    frag = (32 * g + (c >> 2)) * C + 16 * half + 4 * (c & 3);
-    frag2 = ((first_col >> 5) ^ (c >> 2));
+    frag = (8 * g + (c >> 2)) * C + 16 * half + 4 * (c & 3);
+    unit = (first_col >> 5) ^ (c >> 2);
   }
-  QL_DEV void copy(uint16_t *stage, int wv, int kt_) const {
+  QL_DEV void copy(int at, int wv, int kt_, int c) const {
     const int kt = __builtin_amdgcn_readfirstlane(kt_);
-    const int64_t at = (int64_t)kt * kBK * ld;
-    const auto r = lrsrc(base + at, bytes - at * 2);
-#pragma unroll
-    for (int c = 0; c < kCopies; ++c)
-      lload_lds(r, stage + (wv * kCopies + c) * 512, voff[c & 1], (c & ~1) * step);
+    lload_lds(rsrc, at + (wv * kCopies + c) * 1024, voff[c & 1], kt * stride + (c & ~1) * step);
   }
   // the first column's unit is a multiple of the wave's TA or TB (a power of two), so
   // unit + t is unit ^ t and the swizzle of tile t is the lane's with t XORed in
   QL_DEV u32x4 read(const uint16_t *stage, int, int t, int kk) const {
-    const uint16_t *lo = stage + frag + 8 * kk * C + ((frag2 ^ t) << 5);
+    const uint16_t *lo = stage + frag + 16 * kk * C + ((unit ^ t) << 5);
     return ltr_pair(lo, lo + 4 * C);
   }
 };
 
-// acc[i][j] += sum over nk steps of A tile i times B tile j.  S slots of OpA::kElems +
+// acc[i][j] += sum over nk stages of A tile i times B tile j.  S slots of OpA::kElems +
 // OpB::kElems elements at `ring`.
-template <int S, int TA, int TB, typename OpA, typename OpB>
+template <int S, int BK, int TA, int TB, typename OpA, typename OpB>
 QL_DEV void product(const OpA &A, const OpB &B, uint16_t *ring, int nk, int lane, int wv, f32x16 (&acc)[TA][TB]) {
   constexpr int kStage = OpA::kElems + OpB::kElems;
   constexpr int NC = OpA::kCopies + OpB::kCopies;
-  constexpr int kReadsA = std::is_same_v<OpA, RowOperand<OpA::kElems / kBK>> ? 1 : 2;
-  constexpr int kReadsB = std::is_same_v<OpB, RowOperand<OpB::kElems / kBK>> ? 1 : 2;
-  constexpr int NM = TA * TB, NR = TA * kReadsA + TB * kReadsB;
+  constexpr int NG = BK / 16, NM = TA * TB, NF = TA + TB;  // groups; MFMAs and fragments of each
+  static_assert(S * NC < 64, "vmcnt");
   u32x4 fa[2][TA], fb[2][TB];
-  auto copy = [&](int kt, int slot) {
-    A.copy(ring + slot * kStage, wv, kt);
-    B.copy(ring + slot * kStage + OpA::kElems, wv, kt);
+  // Part q of NQ of a stage's copies.  With more than two slots they are spread over the
+  // groups: part 0 follows the barrier that frees the slot, the others ride on the next
+  // stage's groups before its barrier.  Issued at once by all four waves they queue at
+  // the address unit.
+  constexpr int NQ = S > 2 && NC % NG == 0 ? NG : 1;
+  const int base = __builtin_amdgcn_readfirstlane(
+      (int)(uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint16_t *)ring);
+  auto copy1 = [&](int kt, int slot, int c) {
+    if (c < OpA::kCopies) A.copy(base + slot * kStage * 2, wv, kt, c);
+    else B.copy(base + (slot * kStage + OpA::kElems) * 2, wv, kt, c - OpA::kCopies);
   };
-  auto read = [&](int slot, int kk, int set) {
-#pragma unroll
-    for (int i = 0; i < TA; ++i) fa[set][i] = A.read(ring + slot * kStage, lane, i, kk);
-#pragma unroll
-    for (int j = 0; j < TB; ++j) fb[set][j] = B.read(ring + slot * kStage + OpA::kElems, lane, j, kk);
+  auto read = [&](int slot, int kk, int set, int f) {  // fragment f: A's, then B's
+    if (f < TA) fa[set][f] = A.read(ring + slot * kStage, lane, f, kk);
+    else fb[set][f - TA] = B.read(ring + slot * kStage + OpA::kElems, lane, f - TA, kk);
   };
   // vmcnt(n) and lgkmcnt(0)
   auto wait = [](auto nconst) {
@@ -164,34 +185,40 @@ QL_DEV void product(const OpA &A, const OpB &B, uint16_t *ring, int nk, int lane
     __builtin_amdgcn_s_waitcnt((n & 15) | (7 << 4) | ((n >> 4) << 14));
   };
 #pragma unroll
-  for (int s = 0; s < S; ++s) copy(s, s);
+  for (int s = 0; s < S; ++s)
+#pragma unroll
+    for (int c = 0; c < (s < S - 1 ? NC : NC / NQ); ++c) copy1(s, s, c);
   __builtin_amdgcn_sched_barrier(0);
-  wait(std::integral_constant<int, (S - 1) * NC>{});  // stage 0's copies
+  wait(std::integral_constant<int, (S - 2) * NC + NC / NQ>{});  // stage 0's copies
   lbarrier();
   __builtin_amdgcn_sched_barrier(0);
-  read(0, 0, 0);
+#pragma unroll
+  for (int f = 0; f < NF; ++f) read(0, 0, 0, f);
   auto step = [&](auto slotc, int kt) {
     constexpr int SLOT = decltype(slotc)::value;
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      if (kk < 3) {
-        read(SLOT, kk + 1, (kk + 1) & 1);
-      } else {
-        copy(kt + S, SLOT);
-        read((SLOT + 1) % S, 0, 0);
-      }
+    for (int kk = 0; kk < NG; ++kk) {
+      // the next group's reads ride on this group's first half, so that they are done by
+      // its end; the copies are spread over all of it
+      constexpr int RP = (2 * NF + NM - 1) / NM, V = NC / NQ, VP = (V + NM - 1) / NM, GAP = V < NM ? NM / V : 1;
+      const bool last = kk == NG - 1;
+      const bool copies = last || NQ > 1;
 #pragma unroll
-      for (int i = 0; i < TA; ++i)
+      for (int m = 0; m < NM; ++m) {
+        const int i = m / TB, j = m % TB;
+        acc[i][j] = lmfma(fa[kk & 1][i], fb[kk & 1][j], acc[i][j]);
 #pragma unroll
-        for (int j = 0; j < TB; ++j) acc[i][j] = lmfma(fa[kk & 1][i], fb[kk & 1][j], acc[i][j]);
+        for (int f = RP * m; f < RP * (m + 1); ++f)
+          if (f < NF) read(last ? (SLOT + 1) % S : SLOT, last ? 0 : kk + 1, (kk + 1) & 1, f);
+        if (copies && m % GAP == GAP - 1)
 #pragma unroll
-      for (int i = 0; i < NM; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                                          // MFMA
-        if (kk == 3 && i < NC) __builtin_amdgcn_sched_group_barrier(0x010, (NC + NM - 1) / NM, 0);  // VMEM
-        __builtin_amdgcn_sched_group_barrier(0x100, (NR + NM - 1) / NM, 0);                         // LDS read
+          for (int c = VP * (m / GAP); c < VP * (m / GAP + 1); ++c)
+            if (c < V) copy1(last ? kt + S : kt + S - 1, last ? SLOT : (SLOT + S - 1) % S,
+                             (last ? 0 : kk + 1) * V + c);
+        __builtin_amdgcn_sched_barrier(0);
       }
       __builtin_amdgcn_sched_barrier(0);
-      if (kk == 2) {
+      if (kk == NG - 2) {
         // this wave's copies of stage kt + 1 (S - 2 younger stages may be in flight) and
         // its reads of this slot; with that in every wave, stage kt + 1 is whole and the
         // slot is free
@@ -207,14 +234,24 @@ QL_DEV void product(const OpA &A, const OpB &B, uint16_t *ring, int nk, int lane
     step(std::integral_constant<int, 1>{}, kt + 1);
     if constexpr (S > 2) step(std::integral_constant<int, 2 % S>{}, kt + 2);
     if constexpr (S > 3) step(std::integral_constant<int, 3 % S>{}, kt + 3);
+    if constexpr (S > 4) step(std::integral_constant<int, 4 % S>{}, kt + 4);
   }
   if (kt < nk) step(std::integral_constant<int, 0>{}, kt);
   if constexpr (S > 2)
     if (kt + 1 < nk) step(std::integral_constant<int, 1>{}, kt + 1);
   if constexpr (S > 3)
-    if (kt + 2 < nk) step(std::integral_constant<int, 2>{}, kt + 2);
+    if (kt + 2 < nk) step(std::integral_constant<int, 2 % S>{}, kt + 2);
+  if constexpr (S > 4)
+    if (kt + 3 < nk) step(std::integral_constant<int, 3 % S>{}, kt + 3);
   __builtin_amdgcn_s_waitcnt(0);  // no copy of a stage past the end may still land in LDS
   __syncthreads();
+}
+
+// The longest stretch of k that a column operand with rows of ld values takes with 32-bit
+// offsets, its copies past the end included.
+QL_DEV int64_t col_segment(int64_t ld) {
+  const int64_t k = (((int64_t)1 << 31) - 16) / (2 * ld) - 512;
+  return k < 64 ? 64 : k / 64 * 64;
 }
 
 template <int TA, int TB>
@@ -240,10 +277,10 @@ QL_DEV int acc_row(int v, int g) { return 8 * (v >> 2) + 4 * g + (v & 3); }
 // GRAD false: part[tile][token] = (max, sum of exp(z - max)) over the tile's rows, and
 // zlab of the tokens whose label is among them.
 // GRAD true: G[token][v] = bf16((exp(z - lse) - [v is the label]) * (dloss / top)).
-template <int BV, int BT, int WV, int S, bool GRAD>
+template <int BV, int BT, int WV, int S, int BK, bool GRAD>
 __global__ __launch_bounds__(kThreads) void head_logits_kernel(LogitParams p) {
   constexpr int WT = 4 / WV, TA = BV / WV / 32, TB = BT / WT / 32;
-  constexpr int kRing = S * (BV + BT) * kBK;       // elements
+  constexpr int kRing = S * (BV + BT) * BK;        // elements
   constexpr int kLdg = BV + 8;                     // staging of G: [token][BV]
   constexpr int kBytes = lmax(kRing * 2, GRAD ? BT * kLdg * 2 : WV * BT * 8);
   __shared__ __attribute__((aligned(16))) char lds[kBytes];
@@ -257,13 +294,13 @@ __global__ __launch_bounds__(kThreads) void head_logits_kernel(LogitParams p) {
   gemm_tile_of(blockIdx.x, p.tiles_v, tiles_t, 4, tv, tt);
   const int64_t v0 = (int64_t)tv * BV, t0 = (int64_t)tt * BT;
   const int wa = wv / WT * (BV / WV), wb = wv % WT * (BT / WT);  // the wave's first row and column
-  RowOperand<BV> A;
-  RowOperand<BT> B;
+  RowOperand<BV, BK> A;
+  RowOperand<BT, BK> B;
   A.init(p.W + v0 * p.h, p.h, (p.nvoc - v0) * p.h * 2, lane, wv, wa);
   B.init(p.H + t0 * p.h, p.h, ((int64_t)n - t0) * p.h * 2, lane, wv, wb);
   f32x16 acc[TA][TB];
   clear(acc);
-  product<S, TA, TB>(A, B, ring, (int)(p.h / kBK), lane, wv, acc);
+  product<S, BK, TA, TB>(A, B, ring, (int)(p.h / BK), lane, wv, acc);
 
   const int rows = (int)(p.nvoc - v0 < BV ? p.nvoc - v0 : BV);  // vocabulary rows of this tile
   if constexpr (!GRAD) {
@@ -344,11 +381,11 @@ __global__ __launch_bounds__(kThreads) void head_logits_kernel(LogitParams p) {
 // dH partial sums: part[split][token][k] (+)= sum over the split's vocabulary entries v
 // of G[token][v] W[v][k].  G's columns past the piece are zero and W's rows past it read
 // as zero, so the last step may be short.
-template <int BM, int S>
+template <int BM, int S, int BK>
 __global__ __launch_bounds__(kThreads) void head_dh_kernel(HeadGradParams p) {
   constexpr int BN = 256, WM = BM == 256 ? 2 : 1, WN = 4 / WM;
   constexpr int TA = BM / WM / 32, TB = BN / WN / 32;
-  __shared__ __attribute__((aligned(16))) uint16_t ring[S * (BM + BN) * kBK];
+  __shared__ __attribute__((aligned(16))) uint16_t ring[S * (BM + BN) * BK];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 5, l32 = lane & 31;
   const int n = *p.count;
@@ -360,13 +397,17 @@ __global__ __launch_bounds__(kThreads) void head_dh_kernel(HeadGradParams p) {
   const int64_t k0 = (int64_t)blockIdx.y * p.kper;
   const int64_t k1 = k0 + p.kper < p.nvoc ? k0 + p.kper : p.nvoc;
   const int wa = wv / WN * (BM / WM), wb = wv % WN * (BN / WN);
-  RowOperand<BM> A;
-  ColOperand<BN> B;
-  A.init(p.G + m0 * p.ldg + k0, p.ldg, ((int64_t)n - m0) * p.ldg * 2 - k0 * 2, lane, wv, wa);
-  B.init(p.W + k0 * p.h + n0, p.h, (p.nvoc - k0) * p.h * 2 - n0 * 2, lane, wv, wb);
+  RowOperand<BM, BK> A;
+  ColOperand<BN, BK> B;
   f32x16 acc[TA][TB];
   clear(acc);
-  product<S, TA, TB>(A, B, ring, (int)((k1 - k0 + kBK - 1) / kBK), lane, wv, acc);
+  const int64_t seg = col_segment(p.h);
+  for (int64_t k = k0; k < k1; k += seg) {
+    const int64_t len = k1 - k < seg ? k1 - k : seg;
+    A.init(p.G + m0 * p.ldg + k, p.ldg, ((int64_t)n - m0) * p.ldg * 2 - k * 2, lane, wv, wa);
+    B.init(p.W + k * p.h + n0, p.h, (p.nvoc - k) * p.h * 2 - n0 * 2, lane, wv, wb);
+    product<S, BK, TA, TB>(A, B, ring, (int)((len + BK - 1) / BK), lane, wv, acc);
+  }
   float *out = p.part + (int64_t)blockIdx.y * p.rows * p.h;
 #pragma unroll
   for (int i = 0; i < TA; ++i)
@@ -382,10 +423,10 @@ __global__ __launch_bounds__(kThreads) void head_dh_kernel(HeadGradParams p) {
 }
 
 // dW[v][k] = bf16(top * sum over the tokens of G[token][v] H[token][k]).
-template <int S>
+template <int S, int BK>
 __global__ __launch_bounds__(kThreads) void head_dw_kernel(HeadGradParams p) {
   constexpr int BM = 256, BN = 256, TA = 4, TB = 4, kLdc = BN + 8;
-  constexpr int kBytes = lmax(S * (BM + BN) * kBK * 2, BM * kLdc * 2);
+  constexpr int kBytes = lmax(S * (BM + BN) * BK * 2, BM * kLdc * 2);
   __shared__ __attribute__((aligned(16))) char lds[kBytes];
   uint16_t *ring = reinterpret_cast<uint16_t *>(lds);
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -395,13 +436,17 @@ __global__ __launch_bounds__(kThreads) void head_dw_kernel(HeadGradParams p) {
   gemm_tile_of(blockIdx.x, p.tiles_m, p.tiles_n, 4, tm, tn);
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
   const int wa = wv / 2 * 128, wb = wv % 2 * 128;
-  ColOperand<BM> A;
-  ColOperand<BN> B;
-  A.init(p.G + m0, p.ldg, (int64_t)n * p.ldg * 2 - m0 * 2, lane, wv, wa);
-  B.init(p.H + n0, p.h, (int64_t)n * p.h * 2 - n0 * 2, lane, wv, wb);
+  ColOperand<BM, BK> A;
+  ColOperand<BN, BK> B;
   f32x16 acc[TA][TB];
   clear(acc);
-  product<S, TA, TB>(A, B, ring, (n + kBK - 1) / kBK, lane, wv, acc);
+  const int64_t seg = col_segment(p.h > p.ldg ? p.h : p.ldg);
+  for (int64_t k = 0; k < n; k += seg) {
+    const int64_t len = n - k < seg ? n - k : seg;
+    A.init(p.G + k * p.ldg + m0, p.ldg, (n - k) * p.ldg * 2 - m0 * 2, lane, wv, wa);
+    B.init(p.H + k * p.h + n0, p.h, (n - k) * p.h * 2 - n0 * 2, lane, wv, wb);
+    product<S, BK, TA, TB>(A, B, ring, (int)((len + BK - 1) / BK), lane, wv, acc);
+  }
   uint16_t *cs = reinterpret_cast<uint16_t *>(lds);
   const float top = n > 0 ? *p.top : 0.0f;
 #pragma unroll
@@ -429,40 +474,40 @@ int logit_tile_v(int64_t max_tokens) { return max_tokens <= 128 ? 128 : 256; }
 
 hipError_t launch_logit_stats(LogitParams &p, int64_t max_tokens, hipStream_t st) {
   p.tiles_v = (int)cdiv(p.nvoc, logit_tile_v(max_tokens));
-  if (max_tokens <= 32) return launch(head_logits_kernel<128, 32, 4, 4, false>, (unsigned)p.tiles_v, kThreads, st, p);
+  if (max_tokens <= 32) return launch(head_logits_kernel<128, 32, 4, 4, 64, false>, (unsigned)p.tiles_v, kThreads, st, p);
   if (max_tokens <= 128)
-    return launch(head_logits_kernel<128, 128, 2, 2, false>, (unsigned)p.tiles_v, kThreads, st, p);
-  return launch(head_logits_kernel<256, 256, 2, 2, false>, (unsigned)(p.tiles_v * cdiv(max_tokens, 256)), kThreads, st,
+    return launch(head_logits_kernel<128, 128, 2, 4, 32, false>, (unsigned)p.tiles_v, kThreads, st, p);
+  return launch(head_logits_kernel<256, 256, 2, 5, 32, false>, (unsigned)(p.tiles_v * cdiv(max_tokens, 256)), kThreads, st,
                 p);
 }
 
 hipError_t launch_logit_grad(LogitParams &p, int64_t max_tokens, hipStream_t st) {
   if (max_tokens <= 32) {
     p.tiles_v = (int)cdiv(p.nvoc, 128);
-    return launch(head_logits_kernel<128, 32, 4, 4, true>, (unsigned)p.tiles_v, kThreads, st, p);
+    return launch(head_logits_kernel<128, 32, 4, 4, 64, true>, (unsigned)p.tiles_v, kThreads, st, p);
   }
   if (max_tokens <= 128) {
     p.tiles_v = (int)cdiv(p.nvoc, 128);
-    return launch(head_logits_kernel<128, 128, 2, 2, true>, (unsigned)p.tiles_v, kThreads, st, p);
+    return launch(head_logits_kernel<128, 128, 2, 4, 32, true>, (unsigned)p.tiles_v, kThreads, st, p);
   }
   p.tiles_v = (int)cdiv(p.nvoc, 256);
-  return launch(head_logits_kernel<256, 256, 2, 2, true>, (unsigned)(p.tiles_v * cdiv(max_tokens, 256)), kThreads, st,
+  return launch(head_logits_kernel<256, 256, 2, 5, 32, true>, (unsigned)(p.tiles_v * cdiv(max_tokens, 256)), kThreads, st,
                 p);
 }
 
 hipError_t launch_head_dh(HeadGradParams &p, int splits, int64_t max_tokens, hipStream_t st) {
   p.tiles_n = (int)cdiv(p.h, 256);
   if (max_tokens <= 64)
-    return launch(head_dh_kernel<64, 2>, dim3((unsigned)(cdiv(max_tokens, 64) * p.tiles_n), (unsigned)splits), kThreads,
+    return launch(head_dh_kernel<64, 2, 64>, dim3((unsigned)(cdiv(max_tokens, 64) * p.tiles_n), (unsigned)splits), kThreads,
                   st, p);
-  return launch(head_dh_kernel<256, 2>, dim3((unsigned)(cdiv(max_tokens, 256) * p.tiles_n), (unsigned)splits), kThreads,
+  return launch(head_dh_kernel<256, 5, 32>, dim3((unsigned)(cdiv(max_tokens, 256) * p.tiles_n), (unsigned)splits), kThreads,
                 st, p);
 }
 
 hipError_t launch_head_dw(HeadGradParams &p, hipStream_t st) {
   p.tiles_m = (int)cdiv(p.nvoc, 256);
   p.tiles_n = (int)cdiv(p.h, 256);
-  return launch(head_dw_kernel<2>, (unsigned)(p.tiles_m * p.tiles_n), kThreads, st, p);
+  return launch(head_dw_kernel<5, 32>, (unsigned)(p.tiles_m * p.tiles_n), kThreads, st, p);
 }
 
 }  // namespace ql
