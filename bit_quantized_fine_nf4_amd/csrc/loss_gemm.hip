@@ -25,6 +25,7 @@
 
 #include "gemm.h"
 
+#include <numeric>
 #include <type_traits>
 
 namespace ql {
@@ -155,94 +156,90 @@ struct ColOperand {
   }
 };
 
-// acc[i][j] += sum over nk stages of A tile i times B tile j.  S slots of OpA::kElems +
-// OpB::kElems elements at `ring`.
-template <int S, int BK, int TA, int TB, typename OpA, typename OpB>
+template <typename F, int... I>
+QL_DEV void unrolled(F f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+
+// acc[i][j] += sum over nk stages of A tile i times B tile j.  A's ring has SA slots and
+// B's SB, one after the other at `ring`.
+// Stage kt's slots are free after its barrier.  B's copy of stage kt + SB is issued in its
+// last group, A's of stage kt + SA in the next stage's groups before the next barrier, so
+// the copies are spread: issued at once by all four waves they queue at the address unit
+// and hold up the MFMAs behind them.
+template <int SA, int SB, int BK, int TA, int TB, typename OpA, typename OpB>
 QL_DEV void product(const OpA &A, const OpB &B, uint16_t *ring, int nk, int lane, int wv, f32x16 (&acc)[TA][TB]) {
-  constexpr int kStage = OpA::kElems + OpB::kElems;
-  constexpr int NC = OpA::kCopies + OpB::kCopies;
+  constexpr int CA = OpA::kCopies, CB = OpB::kCopies;
   constexpr int NG = BK / 16, NM = TA * TB, NF = TA + TB;  // groups; MFMAs and fragments of each
-  static_assert(S * NC < 64, "vmcnt");
-  u32x4 fa[2][TA], fb[2][TB];
-  // Part q of NQ of a stage's copies.  With more than two slots they are spread over the
-  // groups: part 0 follows the barrier that frees the slot, the others ride on the next
-  // stage's groups before its barrier.  Issued at once by all four waves they queue at
-  // the address unit.
-  constexpr int NQ = S > 2 && NC % NG == 0 ? NG : 1;
+  constexpr int U = std::lcm(SA, SB);
+  // copies that may be in flight at a stage's barrier, where stage kt + 1 has to be whole:
+  // those issued after the later of its two
+  constexpr int kFly = SB <= SA - 1 ? (SB - 1) * CA + (SB - 2) * CB : (SA - 2) * (CA + CB);
+  static_assert(SA > 2 && SB >= 2 && kFly < 64, "ring depths");
+  uint16_t *ringb = ring + SA * OpA::kElems;
   const int base = __builtin_amdgcn_readfirstlane(
       (int)(uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint16_t *)ring);
-  auto copy1 = [&](int kt, int slot, int c) {
-    if (c < OpA::kCopies) A.copy(base + slot * kStage * 2, wv, kt, c);
-    else B.copy(base + (slot * kStage + OpA::kElems) * 2, wv, kt, c - OpA::kCopies);
+  constexpr int kBaseB = SA * OpA::kElems * 2;
+  u32x4 fa[2][TA], fb[2][TB];
+  auto copy_a = [&](int kt, int slot, int c) { A.copy(base + slot * OpA::kElems * 2, wv, kt, c); };
+  auto copy_b = [&](int kt, int slot, int c) { B.copy(base + kBaseB + slot * OpB::kElems * 2, wv, kt, c); };
+  auto read = [&](int sa, int sb, int kk, int set, int f) {  // fragment f: A's, then B's
+    if (f < TA) fa[set][f] = A.read(ring + sa * OpA::kElems, lane, f, kk);
+    else fb[set][f - TA] = B.read(ringb + sb * OpB::kElems, lane, f - TA, kk);
   };
-  auto read = [&](int slot, int kk, int set, int f) {  // fragment f: A's, then B's
-    if (f < TA) fa[set][f] = A.read(ring + slot * kStage, lane, f, kk);
-    else fb[set][f - TA] = B.read(ring + slot * kStage + OpA::kElems, lane, f - TA, kk);
+  auto sync = []() {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt((kFly & 15) | (7 << 4) | ((kFly >> 4) << 14));  // vmcnt(kFly) lgkmcnt(0)
+    lbarrier();
+    __builtin_amdgcn_sched_barrier(0);
   };
-  // vmcnt(n) and lgkmcnt(0)
-  auto wait = [](auto nconst) {
-    constexpr int n = decltype(nconst)::value;
-    __builtin_amdgcn_s_waitcnt((n & 15) | (7 << 4) | ((n >> 4) << 14));
-  };
+  // the first stages, in the order in which the loop issues the later ones
 #pragma unroll
-  for (int s = 0; s < S; ++s)
+  for (int i = -(SA > SB ? SA : SB); i < 0; ++i) {
+    if (i - 1 + SA >= 0)
 #pragma unroll
-    for (int c = 0; c < (s < S - 1 ? NC : NC / NQ); ++c) copy1(s, s, c);
-  __builtin_amdgcn_sched_barrier(0);
-  wait(std::integral_constant<int, (S - 2) * NC + NC / NQ>{});  // stage 0's copies
-  lbarrier();
-  __builtin_amdgcn_sched_barrier(0);
+      for (int c = 0; c < CA; ++c) copy_a(i - 1 + SA, i - 1 + SA, c);
+    if (i + SB >= 0)
 #pragma unroll
-  for (int f = 0; f < NF; ++f) read(0, 0, 0, f);
-  auto step = [&](auto slotc, int kt) {
-    constexpr int SLOT = decltype(slotc)::value;
+      for (int c = 0; c < CB; ++c) copy_b(i + SB, i + SB, c);
+  }
+  sync();
+#pragma unroll
+  for (int f = 0; f < NF; ++f) read(0, 0, 0, 0, f);
+  auto step = [&](auto ic, int kt) {
+    constexpr int I = decltype(ic)::value, ia = I % SA, ib = I % SB;
 #pragma unroll
     for (int kk = 0; kk < NG; ++kk) {
-      // the next group's reads ride on this group's first half, so that they are done by
-      // its end; the copies are spread over all of it
-      constexpr int RP = (2 * NF + NM - 1) / NM, V = NC / NQ, VP = (V + NM - 1) / NM, GAP = V < NM ? NM / V : 1;
       const bool last = kk == NG - 1;
-      const bool copies = last || NQ > 1;
+      // this group's copies: B's in the last group, a share of A's in the others
+      const int c0 = last ? 0 : CA * kk / (NG - 1), c1 = last ? CB : CA * (kk + 1) / (NG - 1);
+      // the next group's reads ride on this group's first half, so that they are done by
+      // its end
+      constexpr int RP = (2 * NF + NM - 1) / NM;
 #pragma unroll
       for (int m = 0; m < NM; ++m) {
         const int i = m / TB, j = m % TB;
         acc[i][j] = lmfma(fa[kk & 1][i], fb[kk & 1][j], acc[i][j]);
 #pragma unroll
         for (int f = RP * m; f < RP * (m + 1); ++f)
-          if (f < NF) read(last ? (SLOT + 1) % S : SLOT, last ? 0 : kk + 1, (kk + 1) & 1, f);
-        if (copies && m % GAP == GAP - 1)
+          if (f < NF) read(last ? (ia + 1) % SA : ia, last ? (ib + 1) % SB : ib, last ? 0 : kk + 1, (kk + 1) & 1, f);
 #pragma unroll
-          for (int c = VP * (m / GAP); c < VP * (m / GAP + 1); ++c)
-            if (c < V) copy1(last ? kt + S : kt + S - 1, last ? SLOT : (SLOT + S - 1) % S,
-                             (last ? 0 : kk + 1) * V + c);
+        for (int c = c0 + (c1 - c0) * m / NM; c < c0 + (c1 - c0) * (m + 1) / NM; ++c) {
+          if (last) copy_b(kt + SB, ib, c);
+          else copy_a(kt - 1 + SA, (ia + SA - 1) % SA, c);
+        }
         __builtin_amdgcn_sched_barrier(0);
       }
-      __builtin_amdgcn_sched_barrier(0);
-      if (kk == NG - 2) {
-        // this wave's copies of stage kt + 1 (S - 2 younger stages may be in flight) and
-        // its reads of this slot; with that in every wave, stage kt + 1 is whole and the
-        // slot is free
-        wait(std::integral_constant<int, (S - 2) * NC>{});
-        lbarrier();
-        __builtin_amdgcn_sched_barrier(0);
-      }
+      // this wave's copies of stage kt + 1 and its reads of stage kt; with that in every
+      // wave, stage kt + 1 is whole and stage kt's slots are free
+      if (kk == NG - 2) sync();
     }
   };
   int kt = 0;
-  for (; kt + S - 1 < nk; kt += S) {
-    step(std::integral_constant<int, 0>{}, kt);
-    step(std::integral_constant<int, 1>{}, kt + 1);
-    if constexpr (S > 2) step(std::integral_constant<int, 2 % S>{}, kt + 2);
-    if constexpr (S > 3) step(std::integral_constant<int, 3 % S>{}, kt + 3);
-    if constexpr (S > 4) step(std::integral_constant<int, 4 % S>{}, kt + 4);
-  }
-  if (kt < nk) step(std::integral_constant<int, 0>{}, kt);
-  if constexpr (S > 2)
-    if (kt + 1 < nk) step(std::integral_constant<int, 1>{}, kt + 1);
-  if constexpr (S > 3)
-    if (kt + 2 < nk) step(std::integral_constant<int, 2 % S>{}, kt + 2);
-  if constexpr (S > 4)
-    if (kt + 3 < nk) step(std::integral_constant<int, 3 % S>{}, kt + 3);
+  for (; kt + U - 1 < nk; kt += U)
+    unrolled([&](auto ic) { step(ic, kt + decltype(ic)::value); }, std::make_integer_sequence<int, U>{});
+  unrolled([&](auto ic) { if (kt + decltype(ic)::value < nk) step(ic, kt + decltype(ic)::value); },
+           std::make_integer_sequence<int, U - 1>{});
   __builtin_amdgcn_s_waitcnt(0);  // no copy of a stage past the end may still land in LDS
   __syncthreads();
 }
@@ -277,10 +274,10 @@ QL_DEV int acc_row(int v, int g) { return 8 * (v >> 2) + 4 * g + (v & 3); }
 // GRAD false: part[tile][token] = (max, sum of exp(z - max)) over the tile's rows, and
 // zlab of the tokens whose label is among them.
 // GRAD true: G[token][v] = bf16((exp(z - lse) - [v is the label]) * (dloss / top)).
-template <int BV, int BT, int WV, int S, int BK, bool GRAD>
+template <int BV, int BT, int WV, int SA, int SB, int BK, bool GRAD>
 __global__ __launch_bounds__(kThreads) void head_logits_kernel(LogitParams p) {
   constexpr int WT = 4 / WV, TA = BV / WV / 32, TB = BT / WT / 32;
-  constexpr int kRing = S * (BV + BT) * BK;        // elements
+  constexpr int kRing = (SA * BV + SB * BT) * BK;  // elements
   constexpr int kLdg = BV + 8;                     // staging of G: [token][BV]
   constexpr int kBytes = lmax(kRing * 2, GRAD ? BT * kLdg * 2 : WV * BT * 8);
   __shared__ __attribute__((aligned(16))) char lds[kBytes];
@@ -300,7 +297,7 @@ __global__ __launch_bounds__(kThreads) void head_logits_kernel(LogitParams p) {
   B.init(p.H + t0 * p.h, p.h, ((int64_t)n - t0) * p.h * 2, lane, wv, wb);
   f32x16 acc[TA][TB];
   clear(acc);
-  product<S, BK, TA, TB>(A, B, ring, (int)(p.h / BK), lane, wv, acc);
+  product<SA, SB, BK, TA, TB>(A, B, ring, (int)(p.h / BK), lane, wv, acc);
 
   const int rows = (int)(p.nvoc - v0 < BV ? p.nvoc - v0 : BV);  // vocabulary rows of this tile
   if constexpr (!GRAD) {
@@ -381,11 +378,11 @@ __global__ __launch_bounds__(kThreads) void head_logits_kernel(LogitParams p) {
 // dH partial sums: part[split][token][k] (+)= sum over the split's vocabulary entries v
 // of G[token][v] W[v][k].  G's columns past the piece are zero and W's rows past it read
 // as zero, so the last step may be short.
-template <int BM, int S, int BK>
+template <int BM, int SA, int SB, int BK>
 __global__ __launch_bounds__(kThreads) void head_dh_kernel(HeadGradParams p) {
   constexpr int BN = 256, WM = BM == 256 ? 2 : 1, WN = 4 / WM;
   constexpr int TA = BM / WM / 32, TB = BN / WN / 32;
-  __shared__ __attribute__((aligned(16))) uint16_t ring[S * (BM + BN) * BK];
+  __shared__ __attribute__((aligned(16))) uint16_t ring[(SA * BM + SB * BN) * BK];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 5, l32 = lane & 31;
   const int n = *p.count;
@@ -406,7 +403,7 @@ __global__ __launch_bounds__(kThreads) void head_dh_kernel(HeadGradParams p) {
     const int64_t len = k1 - k < seg ? k1 - k : seg;
     A.init(p.G + m0 * p.ldg + k, p.ldg, ((int64_t)n - m0) * p.ldg * 2 - k * 2, lane, wv, wa);
     B.init(p.W + k * p.h + n0, p.h, (p.nvoc - k) * p.h * 2 - n0 * 2, lane, wv, wb);
-    product<S, BK, TA, TB>(A, B, ring, (int)((len + BK - 1) / BK), lane, wv, acc);
+    product<SA, SB, BK, TA, TB>(A, B, ring, (int)((len + BK - 1) / BK), lane, wv, acc);
   }
   float *out = p.part + (int64_t)blockIdx.y * p.rows * p.h;
 #pragma unroll
@@ -423,10 +420,10 @@ __global__ __launch_bounds__(kThreads) void head_dh_kernel(HeadGradParams p) {
 }
 
 // dW[v][k] = bf16(top * sum over the tokens of G[token][v] H[token][k]).
-template <int S, int BK>
+template <int SA, int SB, int BK>
 __global__ __launch_bounds__(kThreads) void head_dw_kernel(HeadGradParams p) {
   constexpr int BM = 256, BN = 256, TA = 4, TB = 4, kLdc = BN + 8;
-  constexpr int kBytes = lmax(S * (BM + BN) * BK * 2, BM * kLdc * 2);
+  constexpr int kBytes = lmax((SA * BM + SB * BN) * BK * 2, BM * kLdc * 2);
   __shared__ __attribute__((aligned(16))) char lds[kBytes];
   uint16_t *ring = reinterpret_cast<uint16_t *>(lds);
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -445,7 +442,7 @@ __global__ __launch_bounds__(kThreads) void head_dw_kernel(HeadGradParams p) {
     const int64_t len = n - k < seg ? n - k : seg;
     A.init(p.G + k * p.ldg + m0, p.ldg, (n - k) * p.ldg * 2 - m0 * 2, lane, wv, wa);
     B.init(p.H + k * p.h + n0, p.h, (n - k) * p.h * 2 - n0 * 2, lane, wv, wb);
-    product<S, BK, TA, TB>(A, B, ring, (int)((len + BK - 1) / BK), lane, wv, acc);
+    product<SA, SB, BK, TA, TB>(A, B, ring, (int)((len + BK - 1) / BK), lane, wv, acc);
   }
   uint16_t *cs = reinterpret_cast<uint16_t *>(lds);
   const float top = n > 0 ? *p.top : 0.0f;
@@ -474,40 +471,40 @@ int logit_tile_v(int64_t max_tokens) { return max_tokens <= 128 ? 128 : 256; }
 
 hipError_t launch_logit_stats(LogitParams &p, int64_t max_tokens, hipStream_t st) {
   p.tiles_v = (int)cdiv(p.nvoc, logit_tile_v(max_tokens));
-  if (max_tokens <= 32) return launch(head_logits_kernel<128, 32, 4, 4, 64, false>, (unsigned)p.tiles_v, kThreads, st, p);
+  if (max_tokens <= 32) return launch(head_logits_kernel<128, 32, 4, 4, 4, 64, false>, (unsigned)p.tiles_v, kThreads, st, p);
   if (max_tokens <= 128)
-    return launch(head_logits_kernel<128, 128, 2, 4, 32, false>, (unsigned)p.tiles_v, kThreads, st, p);
-  return launch(head_logits_kernel<256, 256, 2, 5, 32, false>, (unsigned)(p.tiles_v * cdiv(max_tokens, 256)), kThreads, st,
+    return launch(head_logits_kernel<128, 128, 2, 3, 2, 64, false>, (unsigned)p.tiles_v, kThreads, st, p);
+  return launch(head_logits_kernel<256, 256, 2, 3, 2, 64, false>, (unsigned)(p.tiles_v * cdiv(max_tokens, 256)), kThreads, st,
                 p);
 }
 
 hipError_t launch_logit_grad(LogitParams &p, int64_t max_tokens, hipStream_t st) {
   if (max_tokens <= 32) {
     p.tiles_v = (int)cdiv(p.nvoc, 128);
-    return launch(head_logits_kernel<128, 32, 4, 4, 64, true>, (unsigned)p.tiles_v, kThreads, st, p);
+    return launch(head_logits_kernel<128, 32, 4, 4, 4, 64, true>, (unsigned)p.tiles_v, kThreads, st, p);
   }
   if (max_tokens <= 128) {
     p.tiles_v = (int)cdiv(p.nvoc, 128);
-    return launch(head_logits_kernel<128, 128, 2, 4, 32, true>, (unsigned)p.tiles_v, kThreads, st, p);
+    return launch(head_logits_kernel<128, 128, 2, 3, 2, 64, true>, (unsigned)p.tiles_v, kThreads, st, p);
   }
   p.tiles_v = (int)cdiv(p.nvoc, 256);
-  return launch(head_logits_kernel<256, 256, 2, 5, 32, true>, (unsigned)(p.tiles_v * cdiv(max_tokens, 256)), kThreads, st,
+  return launch(head_logits_kernel<256, 256, 2, 3, 2, 64, true>, (unsigned)(p.tiles_v * cdiv(max_tokens, 256)), kThreads, st,
                 p);
 }
 
 hipError_t launch_head_dh(HeadGradParams &p, int splits, int64_t max_tokens, hipStream_t st) {
   p.tiles_n = (int)cdiv(p.h, 256);
   if (max_tokens <= 64)
-    return launch(head_dh_kernel<64, 2, 64>, dim3((unsigned)(cdiv(max_tokens, 64) * p.tiles_n), (unsigned)splits), kThreads,
+    return launch(head_dh_kernel<64, 3, 2, 64>, dim3((unsigned)(cdiv(max_tokens, 64) * p.tiles_n), (unsigned)splits), kThreads,
                   st, p);
-  return launch(head_dh_kernel<256, 5, 32>, dim3((unsigned)(cdiv(max_tokens, 256) * p.tiles_n), (unsigned)splits), kThreads,
+  return launch(head_dh_kernel<256, 3, 2, 64>, dim3((unsigned)(cdiv(max_tokens, 256) * p.tiles_n), (unsigned)splits), kThreads,
                 st, p);
 }
 
 hipError_t launch_head_dw(HeadGradParams &p, hipStream_t st) {
   p.tiles_m = (int)cdiv(p.nvoc, 256);
   p.tiles_n = (int)cdiv(p.h, 256);
-  return launch(head_dw_kernel<5, 32>, (unsigned)(p.tiles_m * p.tiles_n), kThreads, st, p);
+  return launch(head_dw_kernel<5, 5, 32>, (unsigned)(p.tiles_m * p.tiles_n), kThreads, st, p);
 }
 
 }  // namespace ql
