@@ -30,8 +30,8 @@ struct LogitParams {
   int64_t h;
   int64_t v0, nvoc;     // this piece of the vocabulary
   int tiles_v;          // ceil(nvoc / tile rows)
-  // statistics: the piece's max and sum of exponentials per tile row of the vocabulary
-  f32x2 *part;          // [tiles_v][ldp]
+  // statistics: max and sum of exponentials per 128 vocabulary rows (sum 0: no rows)
+  f32x2 *part;          // [ceil(nvoc / 128), even for 256-row tiles][ldp]
   int64_t ldp;
   float *zlab;          // [n] the label's logit
   // gradient: G = (exp(z - lse) - onehot) * (dloss / top)
@@ -40,10 +40,12 @@ struct LogitParams {
   uint16_t *G;          // [n][ldg] bf16, ldg = tiles_v * 256; zero past nvoc
   int64_t ldg;
 };
-// max_tokens bounds n and sizes the grid
+// max_tokens bounds n and chooses the tiles
 hipError_t launch_logit_stats(LogitParams &p, int64_t max_tokens, hipStream_t st);
 hipError_t launch_logit_grad(LogitParams &p, int64_t max_tokens, hipStream_t st);
-int logit_tile_v(int64_t max_tokens);  // vocabulary rows per statistics tile
+hipError_t launch_logit_wide(LogitParams &p, bool grad, hipStream_t st);  // 256 x 256 tiles
+bool logits_wide(int64_t max_tokens, int64_t h);
+int logit_parts(int64_t max_tokens, int64_t h, int64_t V);  // rows of part
 
 struct HeadGradParams {
   const uint16_t *G;   // [n][ldg]
@@ -53,14 +55,32 @@ struct HeadGradParams {
   const int *count;
   const float *top;    // dW: G's common factor
   int64_t h, nvoc;
-  int tiles_m, tiles_n;
-  int64_t kper;        // dH: vocabulary entries per split (a multiple of 64)
-  float *part;         // dH: [splits][rows][h] float32
-  int64_t rows;
+  int tiles_n;
+  int64_t first;       // dH: entries of the first piece, which set the splits
+  int64_t kper;        // dH for at most 64 tokens: vocabulary entries per split
+  float *part;         // dH: [splits][n][h] float32 (at most 64 tokens: [splits][rows][h])
+  int64_t rows;        // rows of h that part has room for in all (at most 64 tokens: M)
   int add;             // dH: add to what part holds (pieces after the first)
   uint16_t *dW;        // dW: [nvoc][h]
 };
-hipError_t launch_head_dh(HeadGradParams &p, int splits, int64_t max_tokens, hipStream_t st);
+hipError_t launch_head_dh(HeadGradParams &p, int64_t max_tokens, hipStream_t st);
+hipError_t launch_head_dh_wide(HeadGradParams &p, hipStream_t st);
 hipError_t launch_head_dw(HeadGradParams &p, hipStream_t st);
+
+// Splits of dH's sum over a piece of the vocabulary, for n tokens on 256 x 256 tiles: the
+// count in 1..16 that leaves the 256 persistent workgroups idle the least, counting a
+// split's partial sums as 4 % of a round of whole tiles.  Host and device choose alike: n
+// is known on the device only.  `rows`: how many rows of partial sums there is room for.
+__host__ __device__ inline int head_splits(int64_t n, int64_t h, int64_t piece, int64_t rows) {
+  const int64_t tiles = (n + 255) / 256 * ((h + 255) / 256), blocks = (piece + 63) / 64;
+  int best = 1;
+  int64_t cost = 0;
+  for (int s = 1; s <= 16 && (s == 1 || (blocks >= 8 * s && s * n <= rows)); ++s) {
+    // rounds of 1 / s tile each, in units of 1 / 10000 of a tile
+    const int64_t c = (tiles * s + 255) / 256 * 10000 / s + 400 * s * tiles / 256;
+    if (s == 1 || c < cost) cost = c, best = s;
+  }
+  return best;
+}
 
 }  // namespace ql

@@ -134,6 +134,7 @@ __global__ __launch_bounds__(256) void loss_finish_kernel(const f32x2 *part, int
   float mx = -__builtin_inff(), s = 0.0f;
   for (int t = lane; t < tiles; t += 64) {
     const f32x2 a = part[(int64_t)t * ldp + i];
+    if (a[1] == 0.0f) continue;  // no rows of the vocabulary
     const float m = fmaxf(mx, a[0]);
     s = s * __expf(mx - m) + a[1] * __expf(a[0] - m);
     mx = m;
@@ -152,17 +153,23 @@ __global__ __launch_bounds__(256) void loss_finish_kernel(const f32x2 *part, int
 }
 
 // dH[idx[i]] = bf16(top * sum over the splits of part[split][i]), eight values per thread.
-__global__ __launch_bounds__(256) void loss_dh_kernel(const float *part, int splits, int64_t rows, int64_t h,
-                                                      const int *count, const int *idx, const float *c_top,
-                                                      uint16_t *dH) {
+// splits 0: as head_splits chooses for the tokens there are, [splits][n][h]; otherwise
+// [splits][M][h].
+__global__ __launch_bounds__(256) void loss_dh_kernel(const float *part, int splits, int64_t M, int64_t rows,
+                                                      int64_t first, int64_t h, const int *count, const int *idx,
+                                                      const float *c_top, uint16_t *dH) {
+  const int n = *count;
+  if (n == 0) return;
   const float top = *c_top;
-  const int64_t per = h / 8, total = (int64_t)*count * per;
+  const int64_t stride = (splits ? M : n) * h;
+  if (!splits) splits = head_splits(n, h, first, rows);
+  const int64_t per = h / 8, total = (int64_t)n * per;
   for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
     const int64_t i = e / per, c = e % per * 8;
     const float *src = part + i * h + c;
     f32x4 a = *reinterpret_cast<const f32x4 *>(src), b = *reinterpret_cast<const f32x4 *>(src + 4);
     for (int s = 1; s < splits; ++s) {
-      const float *q = src + (int64_t)s * rows * h;
+      const float *q = src + (int64_t)s * stride;
       a += *reinterpret_cast<const f32x4 *>(q);
       b += *reinterpret_cast<const f32x4 *>(q + 4);
     }
@@ -184,22 +191,20 @@ int64_t loss_piece(int64_t M, int64_t V) {
   return p < all ? p : all;
 }
 
-// Splits of dH's sum over the vocabulary: the count in 1..16 that leaves the 256 compute
-// units idle the least, counting a split's partial sums as 4 % of a whole pass.
-int loss_splits(int64_t M, int64_t h, int64_t piece) {
-  const int64_t tiles = (M <= 64 ? 1 : cdiv(M, 256)) * cdiv(h, 256);
-  int best = 1;
-  double cost = 1e30;
-  for (int s = 1; s <= 16 && (s == 1 || piece / s >= 512); ++s) {
-    const double c = (double)cdiv(tiles * s, 256) / s + 0.04 * s * (double)tiles / 256;
-    if (c < cost - 1e-9) cost = c, best = s;
-  }
-  return best;
+// At most 64 tokens: splits of dH's sum over the vocabulary until about 512 workgroups
+// read the head, each at least 512 entries of it.
+int few_splits(int64_t h, int64_t piece) {
+  int64_t s = cdiv(512, cdiv(h, 256));
+  s = s > piece / 512 ? piece / 512 : s;
+  return (int)(s < 1 ? 1 : s);
 }
+
+// Rows of partial sums: every token once, and room to split few tokens' sums.
+int64_t partial_rows(int64_t M) { return M > 4096 ? M : (16 * M < 4096 ? 16 * M : 4096); }
 
 struct LossLayout {
   size_t count, top, idx, label, lse, dloss, hc, stat, zlab, g, part, total;
-  int64_t piece, kper;
+  int64_t piece, kper, rows;  // kper and splits: at most 64 tokens
   int splits;
 };
 
@@ -213,17 +218,20 @@ LossLayout loss_layout(int64_t M, int64_t h, int64_t V, bool bwd) {
   L.label = take((size_t)M * 4);
   L.hc = take((size_t)M * h * 2);
   if (!bwd) {
-    L.stat = take((size_t)cdiv(V, logit_tile_v(M)) * M * 8);
+    L.stat = take((size_t)logit_parts(M, h, V) * M * 8);
     L.zlab = take((size_t)M * 4);
   } else {
     L.lse = take((size_t)M * 4);
     L.dloss = take((size_t)M * 4);
     L.piece = loss_piece(M, V);
-    L.splits = loss_splits(M, h, L.piece);
-    L.kper = cdiv(cdiv(L.piece, L.splits), kBlock) * kBlock;
-    L.splits = (int)cdiv(V < L.piece ? V : L.piece, L.kper);  // those that the first piece fills
     L.g = take((size_t)M * L.piece * 2);
-    L.part = take((size_t)L.splits * M * h * 4);
+    L.rows = partial_rows(M);
+    if (M <= 64) {
+      L.kper = cdiv(cdiv(L.piece, few_splits(h, L.piece)), 64) * 64;
+      L.splits = (int)cdiv(V < L.piece ? V : L.piece, L.kper);  // those that the first piece fills
+      L.rows = (int64_t)L.splits * M;
+    }
+    L.part = take((size_t)L.rows * h * 4);
   }
   L.total = off;
   return L;
@@ -261,7 +269,8 @@ hipError_t launch_loss_fwd(const LossArgs &a, float *loss, float *lse, void *ws,
   p.part = at<f32x2>(ws, L.stat), p.ldp = a.M, p.zlab = at<float>(ws, L.zlab);
   e = launch_logit_stats(p, a.M, st);
   if (e != hipSuccess) return e;
-  return launch(loss_finish_kernel, (unsigned)cdiv(a.M, 4), 256, st, (const f32x2 *)p.part, p.ldp, p.tiles_v,
+  return launch(loss_finish_kernel, (unsigned)cdiv(a.M, 4), 256, st, (const f32x2 *)p.part, p.ldp,
+                logit_parts(a.M, a.h, a.V),
                 (const int *)count, (const int *)idx, (const float *)p.zlab, loss, lse);
 }
 
@@ -287,9 +296,10 @@ hipError_t launch_loss_bwd(const LossArgs &a, const float *lse, const float *dlo
     if (e != hipSuccess) return e;
     HeadGradParams q{};
     q.G = p.G, q.ldg = L.piece, q.W = p.W, q.H = Hc, q.count = count, q.top = top, q.h = a.h, q.nvoc = nvoc;
-    q.kper = L.kper, q.part = part, q.rows = a.M, q.add = v0 > 0;
-    // the last piece may fill fewer splits: the others' sums are whole already
-    e = launch_head_dh(q, (int)cdiv(nvoc, L.kper), a.M, st);
+    q.kper = L.kper, q.part = part, q.rows = a.M <= 64 ? a.M : L.rows, q.add = v0 > 0;
+    q.first = a.V < L.piece ? a.V : L.piece;
+    // (at most 64 tokens: the last piece may fill fewer splits; the others' sums are whole)
+    e = launch_head_dh(q, a.M, st);
     if (e != hipSuccess) return e;
     if (dW) {
       q.dW = dW + v0 * a.h;
@@ -299,7 +309,7 @@ hipError_t launch_loss_bwd(const LossArgs &a, const float *lse, const float *dlo
   }
   const int64_t groups = cdiv(a.M * (a.h / 8), 256);
   return launch(loss_dh_kernel, (unsigned)(groups < 8192 ? groups : 8192), 256, st, (const float *)part, L.splits, a.M,
-                a.h, (const int *)count, (const int *)idx, (const float *)top, dH);
+                L.rows, a.V < L.piece ? a.V : L.piece, a.h, (const int *)count, (const int *)idx, (const float *)top, dH);
 }
 
 }  // namespace ql

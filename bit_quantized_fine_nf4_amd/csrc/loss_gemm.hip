@@ -1,8 +1,6 @@
-// The matrix products behind the cross entropy of an output head, for gfx950:
-//   logits  z = H · W^T           (tile of z never leaves the workgroup: it becomes
-//                                  softmax statistics, or the gradient G in bf16)
-//   dH      = G · W               (split over the vocabulary, float32 partial sums)
-//   dW      = G^T · H
+// The products of the output head's cross entropy for few tokens, for gfx950: logits on
+// 128 x 32 and 128 x 128 tiles, dH for at most 64 tokens.  They are bound by reading the
+// head once.  (More tokens, and dW: loss_wide.hip.)
 // One main loop serves all three.  Four waves (one per SIMD) share a tile through LDS;
 // each computes TA x TB MFMA tiles of 32 x 32 (v_mfma_f32_32x32x16_bf16), BK deep per
 // stage.  Both operands go from memory straight into LDS (buffer_load ... lds, 16 bytes
@@ -21,7 +19,7 @@
 // next stage's first reads.
 // Rows past an operand's end read as zero (buffer bounds).
 
-#include "loss.h"
+#include "loss_tiles.h"
 
 #include "gemm.h"
 
@@ -30,131 +28,6 @@
 
 namespace ql {
 namespace {
-
-typedef short ls16x4 __attribute__((ext_vector_type(4)));
-
-// Buffer descriptor over [base, base + bytes), for loads whose rows past the end read zero.
-QL_DEV u32x4 lrsrc(const void *base, int64_t bytes) {
-  const int64_t cap = 0x7FFFFFF0;
-  const uint32_t n = (uint32_t)(bytes < 0 ? 0 : (bytes > cap ? cap : bytes));
-  const uint64_t at = reinterpret_cast<uint64_t>(base);
-  return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)at),
-               (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)(at >> 32) & 0xFFFFu)),
-               (uint32_t)__builtin_amdgcn_readfirstlane((int)n), 0x00020000u};
-}
-QL_DEV f32x16 lmfma(u32x4 a, u32x4 b, f32x16 c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
-                                                0, 0);
-}
-// 16 bytes per lane from a buffer straight into LDS: lane L's bytes land at LDS address
-// at + 16 L; at and soff are the wave's.  It has no register result, so nothing of the compiler's is in
-// flight with it; its completion is awaited by the kernel's own vmcnt waits.  It is written
-// in assembly because the compiler, which knows of the builtin that some LDS is being
-// written, waits for every outstanding copy before each transposing LDS read: with it the
-// dH and dW products of 4096 tokens x 8192 x 32000 took 2.4 and 2.2 ms.  (m0 is a reserved
-// register that the compiler writes right before each use of its own; these kernels have
-// none.)
-QL_DEV void lload_lds(u32x4 rsrc, int at, int voff, int soff) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-               :
-               : "s"(at), "v"(voff), "s"(rsrc), "s"(soff));
-}
-QL_DEV u32x4 ltr_pair(const uint16_t *lo, const uint16_t *hi) {
-  typedef __attribute__((address_space(3))) ls16x4 lds_s16x4;
-  const ls16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(lo));
-  const ls16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(hi));
-  const u32x2 ua = __builtin_bit_cast(u32x2, a), ub = __builtin_bit_cast(u32x2, b);
-  return u32x4{ua[0], ua[1], ub[0], ub[1]};
-}
-// Workgroup barrier without the fences of __syncthreads(), which would wait for the
-// copies in flight; the loop waits for what it needs itself.
-QL_DEV void lbarrier() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-
-constexpr int kThreads = 256;
-constexpr int kWaves = 4;
-
-// An operand stored in rows: R rows of the tile, k along memory, BK of it per stage.
-// `base`: the tile's first row, `bytes`: from there to the operand's end.  Row r's 16-byte
-// chunks sit at chunk ^ f(r), so that the 16 lanes of a read phase (one chunk of 16
-// consecutive rows) cover the 64 banks once.
-template <int R, int BK>
-struct RowOperand {
-  static constexpr int kElems = R * BK;
-  static constexpr int CH = BK / 8;               // chunks per row
-  static constexpr int kRows = 64 / CH;           // rows per 1 KB copy
-  static constexpr int kBlocks = R / kRows;       // copies per stage
-  static constexpr int kCopies = kBlocks < kWaves ? 1 : kBlocks / kWaves;  // per wave
-  static_assert(kCopies == 1 || kCopies % 2 == 0, "a copy's swizzle depends on its parity");
-  u32x4 rsrc;
-  int voff[2], step;
-  int frag, swz;
-  static QL_DEV int f(int r) { return (r / (16 / CH)) & (CH - 1); }
-  // with fewer copies than waves two waves make the same one: every wave's count of
-  // outstanding copies stays the same
-  static QL_DEV int block(int wv, int c) { return kBlocks < kWaves ? wv % kBlocks : wv * kCopies + c; }
-  QL_DEV void init(const uint16_t *base, int64_t ld, int64_t bytes, int lane, int wv, int first_row) {
-    rsrc = lrsrc(base, bytes);
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int r = kRows * block(wv, c) + lane / CH, lc = (lane % CH) ^ f(r);
-      voff[c] = (int)((r * ld + lc * 8) * 2);
-    }
-    step = __builtin_amdgcn_readfirstlane((int)(kRows * ld * 2));
-    const int r = first_row + (lane & 31);  // MFMA tiles are 32 rows apart: f is the same in all of them
-    frag = r * BK;
-    swz = f(r);
-  }
-  // copy c of stage kt into the slot at LDS address `at`
-  QL_DEV void copy(int at, int wv, int kt_, int c) const {
-    const int kt = __builtin_amdgcn_readfirstlane(kt_);
-    lload_lds(rsrc, at + block(wv, c) * 1024, voff[c & 1], kt * BK * 2 + (c & ~1) * step);
-  }
-  QL_DEV u32x4 read(const uint16_t *stage, int lane, int t, int kk) const {
-    return *reinterpret_cast<const u32x4 *>(stage + frag + t * 32 * BK + (((2 * kk + (lane >> 5)) ^ swz) << 3));
-  }
-};
-
-// An operand stored in columns: C columns of the tile along memory, k down the rows.  A
-// row's 64-byte units sit at unit ^ (k % 4).
-template <int C, int BK>
-struct ColOperand {
-  static constexpr int kElems = C * BK;
-  static constexpr int kCopies = C * BK / 512 / kWaves;
-  static constexpr int kPerCopy = 512 / C;        // rows k per 1 KB copy
-  static constexpr int kLanes = 64 / kPerCopy;    // lanes (16-byte chunks) per row
-  u32x4 rsrc;
-  int voff[2], step, stride;
-  int frag, unit;
-  // rows [0, k) of `base` are within 2^31 bytes (kernels walk longer sums in segments)
-  QL_DEV void init(const uint16_t *base, int64_t ld, int64_t bytes, int lane, int wv, int first_col) {
-    rsrc = lrsrc(base, bytes);
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int k = kPerCopy * (wv * kCopies + c) + lane / kLanes, pc = lane % kLanes;
-      const int lc = (((pc >> 2) ^ (k & 3)) << 2) | (pc & 3);
-      voff[c] = (int)((k * ld + lc * 8) * 2);
-    }
-    step = __builtin_amdgcn_readfirstlane((int)(kPerCopy * ld * 2));
-    stride = __builtin_amdgcn_readfirstlane((int)(BK * ld * 2));
-    const int c = lane & 15, half = (lane >> 4) & 1, g = lane >> 5;
-    frag = (8 * g + (c >> 2)) * C + 16 * half + 4 * (c & 3);
-    unit = (first_col >> 5) ^ (c >> 2);
-  }
-  QL_DEV void copy(int at, int wv, int kt_, int c) const {
-    const int kt = __builtin_amdgcn_readfirstlane(kt_);
-    lload_lds(rsrc, at + (wv * kCopies + c) * 1024, voff[c & 1], kt * stride + (c & ~1) * step);
-  }
-  // the first column's unit is a multiple of the wave's TA or TB (a power of two), so
-  // unit + t is unit ^ t and the swizzle of tile t is the lane's with t XORed in
-  QL_DEV u32x4 read(const uint16_t *stage, int, int t, int kk) const {
-    const uint16_t *lo = stage + frag + 16 * kk * C + ((unit ^ t) << 5);
-    return ltr_pair(lo, lo + 4 * C);
-  }
-};
 
 template <typename F, int... I>
 QL_DEV void unrolled(F f, std::integer_sequence<int, I...>) {
@@ -168,7 +41,8 @@ QL_DEV void unrolled(F f, std::integer_sequence<int, I...>) {
 // the copies are spread: issued at once by all four waves they queue at the address unit
 // and hold up the MFMAs behind them.
 template <int SA, int SB, int BK, int TA, int TB, typename OpA, typename OpB>
-QL_DEV void product(const OpA &A, const OpB &B, uint16_t *ring, int nk, int lane, int wv, f32x16 (&acc)[TA][TB]) {
+QL_DEV void product(const OpA &A, const OpB &B, const u32x4 &ra, const u32x4 &rb, uint16_t *ring, int nk, int lane,
+                    int wv, f32x16 (&acc)[TA][TB]) {
   constexpr int CA = OpA::kCopies, CB = OpB::kCopies;
   constexpr int NG = BK / 16, NM = TA * TB, NF = TA + TB;  // groups; MFMAs and fragments of each
   constexpr int U = std::lcm(SA, SB);
@@ -181,8 +55,8 @@ QL_DEV void product(const OpA &A, const OpB &B, uint16_t *ring, int nk, int lane
       (int)(uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint16_t *)ring);
   constexpr int kBaseB = SA * OpA::kElems * 2;
   u32x4 fa[2][TA], fb[2][TB];
-  auto copy_a = [&](int kt, int slot, int c) { A.copy(base + slot * OpA::kElems * 2, wv, kt, c); };
-  auto copy_b = [&](int kt, int slot, int c) { B.copy(base + kBaseB + slot * OpB::kElems * 2, wv, kt, c); };
+  auto copy_a = [&](int kt, int slot, int c) { A.copy(ra, base + slot * OpA::kElems * 2, wv, kt, c); };
+  auto copy_b = [&](int kt, int slot, int c) { B.copy(rb, base + kBaseB + slot * OpB::kElems * 2, wv, kt, c); };
   auto read = [&](int sa, int sb, int kk, int set, int f) {  // fragment f: A's, then B's
     if (f < TA) fa[set][f] = A.read(ring + sa * OpA::kElems, lane, f, kk);
     else fb[set][f - TA] = B.read(ringb + sb * OpB::kElems, lane, f - TA, kk);
@@ -244,27 +118,7 @@ QL_DEV void product(const OpA &A, const OpB &B, uint16_t *ring, int nk, int lane
   __syncthreads();
 }
 
-// The longest stretch of k that a column operand with rows of ld values takes with 32-bit
-// offsets, its copies past the end included.
-QL_DEV int64_t col_segment(int64_t ld) {
-  const int64_t k = (((int64_t)1 << 31) - 16) / (2 * ld) - 512;
-  return k < 64 ? 64 : k / 64 * 64;
-}
-
-template <int TA, int TB>
-QL_DEV void clear(f32x16 (&acc)[TA][TB]) {
-#pragma unroll
-  for (int i = 0; i < TA; ++i)
-#pragma unroll
-    for (int j = 0; j < TB; ++j)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-}
-
 constexpr int lmax(int a, int b) { return a > b ? a : b; }
-
-// the row of accumulator element v in its 32 x 32 tile
-QL_DEV int acc_row(int v, int g) { return 8 * (v >> 2) + 4 * g + (v & 3); }
 
 }  // namespace
 
@@ -293,11 +147,13 @@ __global__ __launch_bounds__(kThreads) void head_logits_kernel(LogitParams p) {
   const int wa = wv / WT * (BV / WV), wb = wv % WT * (BT / WT);  // the wave's first row and column
   RowOperand<BV, BK> A;
   RowOperand<BT, BK> B;
-  A.init(p.W + v0 * p.h, p.h, (p.nvoc - v0) * p.h * 2, lane, wv, wa);
-  B.init(p.H + t0 * p.h, p.h, ((int64_t)n - t0) * p.h * 2, lane, wv, wb);
+  A.init(p.h, lane, wv, wa);
+  B.init(p.h, lane, wv, wb);
+  const u32x4 ra = lrsrc(p.W + v0 * p.h, (p.nvoc - v0) * p.h * 2);
+  const u32x4 rb = lrsrc(p.H + t0 * p.h, ((int64_t)n - t0) * p.h * 2);
   f32x16 acc[TA][TB];
   clear(acc);
-  product<SA, SB, BK, TA, TB>(A, B, ring, (int)(p.h / BK), lane, wv, acc);
+  product<SA, SB, BK, TA, TB>(A, B, ra, rb, ring, (int)(p.h / BK), lane, wv, acc);
 
   const int rows = (int)(p.nvoc - v0 < BV ? p.nvoc - v0 : BV);  // vocabulary rows of this tile
   if constexpr (!GRAD) {
@@ -375,13 +231,11 @@ __global__ __launch_bounds__(kThreads) void head_logits_kernel(LogitParams p) {
   }
 }
 
-// dH partial sums: part[split][token][k] (+)= sum over the split's vocabulary entries v
+// dH partial sums for at most 64 tokens: part[split][token][k] (+)= sum over the split's vocabulary entries v
 // of G[token][v] W[v][k].  G's columns past the piece are zero and W's rows past it read
 // as zero, so the last step may be short.
-template <int BM, int SA, int SB, int BK>
 __global__ __launch_bounds__(kThreads) void head_dh_kernel(HeadGradParams p) {
-  constexpr int BN = 256, WM = BM == 256 ? 2 : 1, WN = 4 / WM;
-  constexpr int TA = BM / WM / 32, TB = BN / WN / 32;
+  constexpr int BM = 64, BN = 256, TA = 2, TB = 2, SA = 3, SB = 2, BK = 64;
   __shared__ __attribute__((aligned(16))) uint16_t ring[(SA * BM + SB * BN) * BK];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 5, l32 = lane & 31;
@@ -393,17 +247,19 @@ __global__ __launch_bounds__(kThreads) void head_dh_kernel(HeadGradParams p) {
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
   const int64_t k0 = (int64_t)blockIdx.y * p.kper;
   const int64_t k1 = k0 + p.kper < p.nvoc ? k0 + p.kper : p.nvoc;
-  const int wa = wv / WN * (BM / WM), wb = wv % WN * (BN / WN);
+  const int wa = 0, wb = wv * 64;
   RowOperand<BM, BK> A;
   ColOperand<BN, BK> B;
+  A.init(p.ldg, lane, wv, wa);
+  B.init(p.h, lane, wv, wb);
   f32x16 acc[TA][TB];
   clear(acc);
   const int64_t seg = col_segment(p.h);
   for (int64_t k = k0; k < k1; k += seg) {
     const int64_t len = k1 - k < seg ? k1 - k : seg;
-    A.init(p.G + m0 * p.ldg + k, p.ldg, ((int64_t)n - m0) * p.ldg * 2 - k * 2, lane, wv, wa);
-    B.init(p.W + k * p.h + n0, p.h, (p.nvoc - k) * p.h * 2 - n0 * 2, lane, wv, wb);
-    product<SA, SB, BK, TA, TB>(A, B, ring, (int)((len + BK - 1) / BK), lane, wv, acc);
+    const u32x4 ra = lrsrc(p.G + m0 * p.ldg + k, ((int64_t)n - m0) * p.ldg * 2 - k * 2);
+    const u32x4 rb = lrsrc(p.W + k * p.h + n0, (p.nvoc - k) * p.h * 2 - n0 * 2);
+    product<SA, SB, BK, TA, TB>(A, B, ra, rb, ring, (int)((len + BK - 1) / BK), lane, wv, acc);
   }
   float *out = p.part + (int64_t)blockIdx.y * p.rows * p.h;
 #pragma unroll
@@ -419,92 +275,40 @@ __global__ __launch_bounds__(kThreads) void head_dh_kernel(HeadGradParams p) {
       }
 }
 
-// dW[v][k] = bf16(top * sum over the tokens of G[token][v] H[token][k]).
-template <int SA, int SB, int BK>
-__global__ __launch_bounds__(kThreads) void head_dw_kernel(HeadGradParams p) {
-  constexpr int BM = 256, BN = 256, TA = 4, TB = 4, kLdc = BN + 8;
-  constexpr int kBytes = lmax((SA * BM + SB * BN) * BK * 2, BM * kLdc * 2);
-  __shared__ __attribute__((aligned(16))) char lds[kBytes];
-  uint16_t *ring = reinterpret_cast<uint16_t *>(lds);
-  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int g = lane >> 5, l32 = lane & 31;
-  const int n = *p.count;
-  int tm, tn;
-  gemm_tile_of(blockIdx.x, p.tiles_m, p.tiles_n, 4, tm, tn);
-  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
-  const int wa = wv / 2 * 128, wb = wv % 2 * 128;
-  ColOperand<BM, BK> A;
-  ColOperand<BN, BK> B;
-  f32x16 acc[TA][TB];
-  clear(acc);
-  const int64_t seg = col_segment(p.h > p.ldg ? p.h : p.ldg);
-  for (int64_t k = 0; k < n; k += seg) {
-    const int64_t len = n - k < seg ? n - k : seg;
-    A.init(p.G + k * p.ldg + m0, p.ldg, (n - k) * p.ldg * 2 - m0 * 2, lane, wv, wa);
-    B.init(p.H + k * p.h + n0, p.h, (n - k) * p.h * 2 - n0 * 2, lane, wv, wb);
-    product<SA, SB, BK, TA, TB>(A, B, ring, (int)((len + BK - 1) / BK), lane, wv, acc);
-  }
-  uint16_t *cs = reinterpret_cast<uint16_t *>(lds);
-  const float top = n > 0 ? *p.top : 0.0f;
-#pragma unroll
-  for (int i = 0; i < TA; ++i)
-#pragma unroll
-    for (int j = 0; j < TB; ++j)
-#pragma unroll
-      for (int v = 0; v < 16; ++v)
-        cs[(wa + 32 * i + acc_row(v, g)) * kLdc + wb + 32 * j + l32] =
-            (uint16_t)(pack_bf16x2(top * acc[i][j][v], 0.0f) & 0xFFFFu);
-  __syncthreads();
-  for (int ch = threadIdx.x; ch < BM * BN / 8; ch += kThreads) {
-    const int row = ch / (BN / 8), c8 = ch % (BN / 8);
-    const int64_t m = m0 + row, c = n0 + c8 * 8;
-    if (m < p.nvoc && c < p.h)
-      *reinterpret_cast<u32x4 *>(p.dW + m * p.h + c) = *reinterpret_cast<const u32x4 *>(cs + row * kLdc + c8 * 8);
-  }
-}
-
 namespace {
 inline int64_t cdiv(int64_t x, int64_t m) { return (x + m - 1) / m; }
 }  // namespace
 
-int logit_tile_v(int64_t max_tokens) { return max_tokens <= 128 ? 128 : 256; }
+// Tokens from which the 256 x 256 tiles are used: the statistics of 129 tokens fill half
+// of such a tile, 128 fill one of 128 x 128.  They need two stages (h of 64 has one).
+bool logits_wide(int64_t max_tokens, int64_t h) { return max_tokens > 128 && h >= 128; }
+int logit_parts(int64_t max_tokens, int64_t h, int64_t V) {
+  return logits_wide(max_tokens, h) ? 2 * (int)cdiv(V, 256) : (int)cdiv(V, 128);
+}
+
+namespace {
+template <bool GRAD>
+hipError_t logits(LogitParams &p, int64_t max_tokens, hipStream_t st) {
+  if (logits_wide(max_tokens, p.h)) return launch_logit_wide(p, GRAD, st);
+  p.tiles_v = (int)cdiv(p.nvoc, 128);
+  if (max_tokens <= 32)
+    return launch(head_logits_kernel<128, 32, 4, 4, 4, 64, GRAD>, (unsigned)p.tiles_v, kThreads, st, p);
+  return launch(head_logits_kernel<128, 128, 2, 3, 2, 64, GRAD>, (unsigned)(p.tiles_v * cdiv(max_tokens, 128)),
+                kThreads, st, p);
+}
+}  // namespace
 
 hipError_t launch_logit_stats(LogitParams &p, int64_t max_tokens, hipStream_t st) {
-  p.tiles_v = (int)cdiv(p.nvoc, logit_tile_v(max_tokens));
-  if (max_tokens <= 32) return launch(head_logits_kernel<128, 32, 4, 4, 4, 64, false>, (unsigned)p.tiles_v, kThreads, st, p);
-  if (max_tokens <= 128)
-    return launch(head_logits_kernel<128, 128, 2, 3, 2, 64, false>, (unsigned)p.tiles_v, kThreads, st, p);
-  return launch(head_logits_kernel<256, 256, 2, 3, 2, 64, false>, (unsigned)(p.tiles_v * cdiv(max_tokens, 256)), kThreads, st,
-                p);
+  return logits<false>(p, max_tokens, st);
 }
-
 hipError_t launch_logit_grad(LogitParams &p, int64_t max_tokens, hipStream_t st) {
-  if (max_tokens <= 32) {
-    p.tiles_v = (int)cdiv(p.nvoc, 128);
-    return launch(head_logits_kernel<128, 32, 4, 4, 4, 64, true>, (unsigned)p.tiles_v, kThreads, st, p);
-  }
-  if (max_tokens <= 128) {
-    p.tiles_v = (int)cdiv(p.nvoc, 128);
-    return launch(head_logits_kernel<128, 128, 2, 3, 2, 64, true>, (unsigned)p.tiles_v, kThreads, st, p);
-  }
-  p.tiles_v = (int)cdiv(p.nvoc, 256);
-  return launch(head_logits_kernel<256, 256, 2, 3, 2, 64, true>, (unsigned)(p.tiles_v * cdiv(max_tokens, 256)), kThreads, st,
-                p);
+  return logits<true>(p, max_tokens, st);
 }
 
-hipError_t launch_head_dh(HeadGradParams &p, int splits, int64_t max_tokens, hipStream_t st) {
+hipError_t launch_head_dh(HeadGradParams &p, int64_t max_tokens, hipStream_t st) {
+  if (max_tokens > 64) return launch_head_dh_wide(p, st);
   p.tiles_n = (int)cdiv(p.h, 256);
-  if (max_tokens <= 64)
-    return launch(head_dh_kernel<64, 3, 2, 64>, dim3((unsigned)(cdiv(max_tokens, 64) * p.tiles_n), (unsigned)splits), kThreads,
-                  st, p);
-  return launch(head_dh_kernel<256, 3, 2, 64>, dim3((unsigned)(cdiv(max_tokens, 256) * p.tiles_n), (unsigned)splits), kThreads,
-                st, p);
-}
-
-hipError_t launch_head_dw(HeadGradParams &p, hipStream_t st) {
-  p.tiles_m = (int)cdiv(p.nvoc, 256);
-  p.tiles_n = (int)cdiv(p.h, 256);
-  return launch(head_dw_kernel<5, 5, 32>, (unsigned)(p.tiles_m * p.tiles_n), kThreads, st, p);
+  return launch(head_dh_kernel, dim3((unsigned)p.tiles_n, (unsigned)cdiv(p.nvoc, p.kper)), kThreads, st, p);
 }
 
 }  // namespace ql
