@@ -24,7 +24,7 @@ hipError_t launch_loss_bwd(const LossArgs &a, const float *lse, const float *dlo
 // Compact tokens: the n = *count tokens that carry a loss, in order.
 struct LogitParams {
   const uint16_t *W;    // rows v0 .. of the head: [nvoc][h]
-  const uint16_t *H;    // [n][h] compact hidden states
+  const uint16_t *H;    // [n][h] compact hidden states, blocked
   const int *count;     // n (device)
   const int *label;     // [n] labels in the whole vocabulary
   int64_t h;
@@ -37,8 +37,8 @@ struct LogitParams {
   // gradient: G = (exp(z - lse) - onehot) * (dloss / top)
   const float *lse, *dloss;  // [n]
   const float *top;          // the largest |dloss| (device)
-  uint16_t *G;          // [n][ldg] bf16, ldg = tiles_v * 256; zero past nvoc
-  int64_t ldg;
+  uint16_t *G;          // [n][piece], blocked, gblocks blocks per row; zero past nvoc up to
+  int64_t gblocks;      // the next 256 and past n up to the next 32
 };
 // max_tokens bounds n and chooses the tiles
 hipError_t launch_logit_stats(LogitParams &p, int64_t max_tokens, hipStream_t st);
@@ -48,10 +48,10 @@ bool logits_wide(int64_t max_tokens, int64_t h);
 int logit_parts(int64_t max_tokens, int64_t h, int64_t V);  // rows of part
 
 struct HeadGradParams {
-  const uint16_t *G;   // [n][ldg]
-  int64_t ldg;
+  const uint16_t *G;   // [n][piece], blocked
+  int64_t gblocks;     // blocks per row
   const uint16_t *W;   // dH: [nvoc][h] rows of this piece
-  const uint16_t *H;   // dW: [n][h] compact hidden states
+  const uint16_t *H;   // dW: [n][h] compact hidden states, blocked
   const int *count;
   const float *top;    // dW: G's common factor
   int64_t h, nvoc;

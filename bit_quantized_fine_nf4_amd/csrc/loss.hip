@@ -105,20 +105,22 @@ __global__ __launch_bounds__(kSelThreads) void loss_select_kernel(const int64_t 
   }
 }
 
-// Row i of the compact copy = row idx[i] of H (i < n); with dH, the rows without a label
-// become zero.  One wave per row.
+// Row i of the compact copy (blocked) = row idx[i] of H (i < n), zero from n up to the next
+// 32; with dH, the rows without a label become zero.  One wave per row.
 __global__ __launch_bounds__(256) void loss_gather_kernel(const uint16_t *H, int64_t M, int64_t h, const int *count,
                                                           const int *idx, uint16_t *Hc, const int64_t *labels,
                                                           int64_t V, uint16_t *dH) {
   const int lane = threadIdx.x & 63;
-  const int n = *count;
-  for (int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); i < M; i += (int64_t)gridDim.x * 4) {
-    if (i < n) {
-      const u32x4 *src = reinterpret_cast<const u32x4 *>(H + (int64_t)idx[i] * h);
-      u32x4 *dst = reinterpret_cast<u32x4 *>(Hc + i * h);
-      for (int64_t c = lane; c < h / 8; c += 64) dst[c] = src[c];
+  const int n = *count, pad = (n + 31) / 32 * 32;
+  const int64_t rows = M > pad ? M : pad;
+  for (int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); i < rows; i += (int64_t)gridDim.x * 4) {
+    if (i < pad) {
+      const u32x4 *src = reinterpret_cast<const u32x4 *>(H + (int64_t)(i < n ? idx[i] : 0) * h);
+      uint16_t *dst = Hc + (i >> 5) * h * 32 + (i & 31) * 32;
+      for (int64_t c = lane; c < h / 8; c += 64)
+        *reinterpret_cast<u32x4 *>(dst + (c >> 2) * 1024 + (c & 3) * 8) = i < n ? src[c] : u32x4{0, 0, 0, 0};
     }
-    if (dH && (labels[i] < 0 || labels[i] >= V)) {
+    if (dH && i < M && (labels[i] < 0 || labels[i] >= V)) {
       u32x4 *dst = reinterpret_cast<u32x4 *>(dH + i * h);
       for (int64_t c = lane; c < h / 8; c += 64) dst[c] = u32x4{0, 0, 0, 0};
     }
@@ -216,7 +218,8 @@ LossLayout loss_layout(int64_t M, int64_t h, int64_t V, bool bwd) {
   L.top = take(4);
   L.idx = take((size_t)M * 4);
   L.label = take((size_t)M * 4);
-  L.hc = take((size_t)M * h * 2);
+  const int64_t Mp = cdiv(M, 256) * 256;  // the blocked matrices' rows
+  L.hc = take((size_t)Mp * h * 2);
   if (!bwd) {
     L.stat = take((size_t)logit_parts(M, h, V) * M * 8);
     L.zlab = take((size_t)M * 4);
@@ -224,7 +227,7 @@ LossLayout loss_layout(int64_t M, int64_t h, int64_t V, bool bwd) {
     L.lse = take((size_t)M * 4);
     L.dloss = take((size_t)M * 4);
     L.piece = loss_piece(M, V);
-    L.g = take((size_t)M * L.piece * 2);
+    L.g = take((size_t)Mp * L.piece * 2);
     L.rows = partial_rows(M);
     if (M <= 64) {
       L.kper = cdiv(cdiv(L.piece, few_splits(h, L.piece)), 64) * 64;
@@ -291,11 +294,11 @@ hipError_t launch_loss_bwd(const LossArgs &a, const float *lse, const float *dlo
     const int64_t nvoc = a.V - v0 < L.piece ? a.V - v0 : L.piece;
     LogitParams p{};
     p.W = a.W + v0 * a.h, p.H = Hc, p.count = count, p.label = label, p.h = a.h, p.v0 = v0, p.nvoc = nvoc;
-    p.lse = c_lse, p.dloss = c_dl, p.top = top, p.G = at<uint16_t>(ws, L.g), p.ldg = L.piece;
+    p.lse = c_lse, p.dloss = c_dl, p.top = top, p.G = at<uint16_t>(ws, L.g), p.gblocks = L.piece / 32;
     e = launch_logit_grad(p, a.M, st);
     if (e != hipSuccess) return e;
     HeadGradParams q{};
-    q.G = p.G, q.ldg = L.piece, q.W = p.W, q.H = Hc, q.count = count, q.top = top, q.h = a.h, q.nvoc = nvoc;
+    q.G = p.G, q.gblocks = L.piece / 32, q.W = p.W, q.H = Hc, q.count = count, q.top = top, q.h = a.h, q.nvoc = nvoc;
     q.kper = L.kper, q.part = part, q.rows = a.M <= 64 ? a.M : L.rows, q.add = v0 > 0;
     q.first = a.V < L.piece ? a.V : L.piece;
     // (at most 64 tokens: the last piece may fill fewer splits; the others' sums are whole)

@@ -146,11 +146,11 @@ __global__ __launch_bounds__(kThreads) void head_logits_kernel(LogitParams p) {
   const int64_t v0 = (int64_t)tv * BV, t0 = (int64_t)tt * BT;
   const int wa = wv / WT * (BV / WV), wb = wv % WT * (BT / WT);  // the wave's first row and column
   RowOperand<BV, BK> A;
-  RowOperand<BT, BK> B;
+  BlockRows<BT, BK> B;
   A.init(p.h, lane, wv, wa);
-  B.init(p.h, lane, wv, wb);
+  B.init(p.h * 64, lane, wv, wb);
   const u32x4 ra = lrsrc(p.W + v0 * p.h, (p.nvoc - v0) * p.h * 2);
-  const u32x4 rb = lrsrc(p.H + t0 * p.h, ((int64_t)n - t0) * p.h * 2);
+  const u32x4 rb = lrsrc(p.H + t0 * p.h, ((n + 31) / 32 * 32 - t0) * p.h * 2);
   f32x16 acc[TA][TB];
   clear(acc);
   product<SA, SB, BK, TA, TB>(A, B, ra, rb, ring, (int)(p.h / BK), lane, wv, acc);
@@ -223,10 +223,9 @@ __global__ __launch_bounds__(kThreads) void head_logits_kernel(LogitParams p) {
     }
     __syncthreads();
     for (int ch = threadIdx.x; ch < BT * BV / 8; ch += kThreads) {
-      const int col = ch / (BV / 8), c8 = ch % (BV / 8);
-      if (t0 + col < n)
-        *reinterpret_cast<u32x4 *>(p.G + (t0 + col) * p.ldg + v0 + c8 * 8) =
-            *reinterpret_cast<const u32x4 *>(cs + col * kLdg + c8 * 8);
+      const int col = ch / (BV / 8), c8 = ch % (BV / 8);  // tokens past the last: zero, within a whole 32
+      *reinterpret_cast<u32x4 *>(p.G + blocked(t0 + col, v0 + c8 * 8, p.gblocks)) =
+          *reinterpret_cast<const u32x4 *>(cs + col * kLdg + c8 * 8);
     }
   }
 }
@@ -248,16 +247,16 @@ __global__ __launch_bounds__(kThreads) void head_dh_kernel(HeadGradParams p) {
   const int64_t k0 = (int64_t)blockIdx.y * p.kper;
   const int64_t k1 = k0 + p.kper < p.nvoc ? k0 + p.kper : p.nvoc;
   const int wa = 0, wb = wv * 64;
-  RowOperand<BM, BK> A;
+  BlockRows<BM, BK> A;
   ColOperand<BN, BK> B;
-  A.init(p.ldg, lane, wv, wa);
+  A.init(p.gblocks * 2048, lane, wv, wa);
   B.init(p.h, lane, wv, wb);
   f32x16 acc[TA][TB];
   clear(acc);
   const int64_t seg = col_segment(p.h);
   for (int64_t k = k0; k < k1; k += seg) {
     const int64_t len = k1 - k < seg ? k1 - k : seg;
-    const u32x4 ra = lrsrc(p.G + m0 * p.ldg + k, ((int64_t)n - m0) * p.ldg * 2 - k * 2);
+    const u32x4 ra = lrsrc(p.G + (k >> 5) * 1024, (n + 31) / 32 * p.gblocks * 2048 - (k >> 5) * 2048);
     const u32x4 rb = lrsrc(p.W + k * p.h + n0, (p.nvoc - k) * p.h * 2 - n0 * 2);
     product<SA, SB, BK, TA, TB>(A, B, ra, rb, ring, (int)((len + BK - 1) / BK), lane, wv, acc);
   }
@@ -280,8 +279,8 @@ inline int64_t cdiv(int64_t x, int64_t m) { return (x + m - 1) / m; }
 }  // namespace
 
 // Tokens from which the 256 x 256 tiles are used: the statistics of 129 tokens fill half
-// of such a tile, 128 fill one of 128 x 128.  They need two stages (h of 64 has one).
-bool logits_wide(int64_t max_tokens, int64_t h) { return max_tokens > 128 && h >= 128; }
+// of such a tile, 128 fill one of 128 x 128.  They need h of three 64-deep stages.
+bool logits_wide(int64_t max_tokens, int64_t h) { return max_tokens > 128 && h >= 192; }
 int logit_parts(int64_t max_tokens, int64_t h, int64_t V) {
   return logits_wide(max_tokens, h) ? 2 * (int)cdiv(V, 256) : (int)cdiv(V, 128);
 }
@@ -290,7 +289,8 @@ namespace {
 template <bool GRAD>
 hipError_t logits(LogitParams &p, int64_t max_tokens, hipStream_t st) {
   if (logits_wide(max_tokens, p.h)) return launch_logit_wide(p, GRAD, st);
-  p.tiles_v = (int)cdiv(p.nvoc, 128);
+  // G is written (zero past the piece) up to a multiple of 256
+  p.tiles_v = GRAD ? 2 * (int)cdiv(p.nvoc, 256) : (int)cdiv(p.nvoc, 128);
   if (max_tokens <= 32)
     return launch(head_logits_kernel<128, 32, 4, 4, 4, 64, GRAD>, (unsigned)p.tiles_v, kThreads, st, p);
   return launch(head_logits_kernel<128, 128, 2, 3, 2, 64, GRAD>, (unsigned)(p.tiles_v * cdiv(max_tokens, 128)),

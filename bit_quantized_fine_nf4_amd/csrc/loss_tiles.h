@@ -1,19 +1,24 @@
 // Operand tiles of the head's products: copies from memory into LDS and MFMA fragments
 // out of it (loss_gemm.hip, loss_wide.hip).
 //
-// An operand is stored in one of two ways:
-//   rows   k runs along memory: a stage is [rows][BK] with 16-byte chunks XOR-swizzled
-//          by row; a fragment (8 consecutive k of one row) is one 16-byte read;
-//   cols   the tile's own index runs along memory: a stage is [BK][cols] as it is, whose
-//          64-byte units are XOR-swizzled by k % 4; a fragment is two transposing reads
-//          (ds_read_b64_tr_b16), whose 32-lane phases name 4 rows k of one unit and so
-//          cover the 64 banks once.
+// The head W is the caller's row-major [V][h].  The compact hidden states and G live in the
+// workspace and are blocked: 32 x 32 blocks of 2 KB, [token / 32][column / 32][32][32], rows
+// past the last token zero up to the next 32.  A block is a contiguous stretch of whole
+// cache lines whichever of its two indices is summed over.
+//
+// A tile enters a product in one of two ways:
+//   rows   k runs along a row: a stage is [rows][BK] with 16-byte chunks XOR-swizzled by
+//          row; a fragment (8 consecutive k of one row) is one 16-byte read;
+//   cols   k runs down the rows: a fragment is two transposing reads (ds_read_b64_tr_b16),
+//          whose 32-lane phases name 4 rows k of 64 bytes.  A stage of W is [BK][cols] as
+//          it is, with 64-byte units XOR-swizzled by k % 4; a stage of blocks keeps them,
+//          and 4 rows of a block are 256 consecutive bytes.  Either way a phase covers the
+//          64 banks once.
 // MFMA group kk of a stage takes k = 16 kk + 8 (lane / 32) + 0..7 of both operands.  Rows
 // past an operand's end read as zero (buffer bounds).
-// A row operand's stage is 64 deep: 128-byte lines are copied whole.  (32-deep stages, half
-// a line per copy, left a deeper ring but cost twice the cache requests: a copy-only loop
-// moved 15 TB/s in half lines and 28 TB/s in whole ones, the logits of 4096 tokens x 8192 x
-// 32000 took 1.80 instead of 1.62 ms.)
+// W's rows are copied 64 deep, in whole 128-byte lines.  (32-deep stages, half a line per
+// copy, cost twice the cache requests: a copy-only loop moved 15 TB/s in half lines and 28
+// TB/s in whole ones.)
 #pragma once
 
 #include "loss.h"
@@ -106,6 +111,60 @@ struct RowOperand {
   }
 };
 
+// Blocked rows: R tokens of the tile, BK of the blocked columns per stage.  `ldb`: bytes
+// of one row of blocks.
+template <int R, int BK>
+struct BlockRows {
+  static constexpr int kElems = R * BK;
+  static constexpr int CH = BK / 8, kRows = 64 / CH, kBlocks = R / kRows;
+  static constexpr int kCopies = kBlocks < kWaves ? 1 : kBlocks / kWaves;
+  int voff[2], ldb;
+  int frag, swz;
+  static QL_DEV int f(int r) { return RowOperand<R, BK>::f(r); }
+  static QL_DEV int block(int wv, int c) { return RowOperand<R, BK>::block(wv, c); }
+  QL_DEV void init(int64_t ld_bytes, int lane, int wv, int first_row) {
+    ldb = __builtin_amdgcn_readfirstlane((int)ld_bytes);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int r = kRows * block(wv, c) + lane / CH, lc = (lane % CH) ^ f(r);
+      voff[c] = (lc >> 2) * 2048 + (lane / CH) * 64 + (lc & 3) * 16;
+    }
+    const int r = first_row + (lane & 31);
+    frag = r * BK;
+    swz = f(r);
+  }
+  QL_DEV void copy(const u32x4 &rsrc, int at, int wv, int kt_, int c) const {
+    const int kt = __builtin_amdgcn_readfirstlane(kt_), b = block(wv, c);
+    lload_lds(rsrc, at + b * 1024, voff[c & 1],
+              b / (32 / kRows) * ldb + b % (32 / kRows) * (kRows * 64) + kt * (BK / 32) * 2048);
+  }
+  QL_DEV u32x4 read(const uint16_t *stage, int lane, int t, int kk) const {
+    return *reinterpret_cast<const u32x4 *>(stage + frag + t * 32 * BK + (((2 * kk + (lane >> 5)) ^ swz) << 3));
+  }
+};
+
+// Blocked columns: C of the blocked columns along the tile, 32 tokens k per stage.
+template <int C>
+struct BlockCols {
+  static constexpr int kElems = C * 32;
+  static constexpr int kCopies = kElems / 512 / kWaves;
+  int voff, ldb, frag;
+  QL_DEV void init(int64_t ld_bytes, int lane, int, int first_col) {
+    ldb = __builtin_amdgcn_readfirstlane((int)ld_bytes);
+    voff = lane * 16;
+    const int c = lane & 15, half = (lane >> 4) & 1, g = lane >> 5;
+    frag = first_col * 32 + (8 * g + (c >> 2)) * 32 + 16 * half + 4 * (c & 3);
+  }
+  QL_DEV void copy(const u32x4 &rsrc, int at, int wv, int kt_, int c) const {
+    const int kt = __builtin_amdgcn_readfirstlane(kt_);
+    lload_lds(rsrc, at + (wv * kCopies + c) * 1024, voff, kt * ldb + (wv * kCopies + c) * 1024);
+  }
+  QL_DEV u32x4 read(const uint16_t *stage, int, int t, int kk) const {
+    const uint16_t *lo = stage + frag + t * 1024 + kk * 512;
+    return ltr_pair(lo, lo + 128);
+  }
+};
+
 // An operand stored in columns: C columns of the tile along memory, k down the rows.  A
 // row's 64-byte units sit at unit ^ (k % 4).
 template <int C, int BK>
@@ -157,6 +216,11 @@ QL_DEV void clear(f32x16 (&acc)[TA][TB]) {
     for (int j = 0; j < TB; ++j)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+}
+
+// The element (row, col) of a blocked matrix with `blocks` blocks per row.
+QL_DEV int64_t blocked(int64_t row, int64_t col, int64_t blocks) {
+  return ((row >> 5) * blocks + (col >> 5)) * 1024 + (row & 31) * 32 + (col & 31);
 }
 
 // the row of accumulator element v in its 32 x 32 tile

@@ -5,16 +5,19 @@
 //   dW      = G^T · H
 // One persistent workgroup per compute unit: four waves, one per SIMD, 128 x 128 of the
 // tile each (4 x 4 tiles of v_mfma_f32_32x32x16_bf16, 256 accumulator registers), both
-// operands through LDS.  A workgroup walks its list of tiles as one stream of 64-deep
-// stages: the last two stages of a tile copy the first two of the next, so a tile costs
-// neither a cold start nor copies past its end, and its epilogue runs while they land.
+// operands through LDS.  A workgroup walks its list of tiles as one stream of stages: the
+// last stages of a tile copy the first of the next, so a tile costs neither a cold start
+// nor copies past its end, and its epilogue runs while they land.
 //
-// LDS is all ring: three slots for operand A and two for B (160 KB).  Stage kt's slots are
-// free after its barrier, which follows its third group of MFMAs: by then its last
-// fragments are read.  B's copy of stage kt + 2 is issued in the last group, A's in the
-// next stage's groups, so that copies are spread over the stage: issued at once by all
-// four waves they queue at the address unit and hold up the MFMAs behind them.  The
-// barrier waits for the copies of stage kt + 1 and lets A's of stage kt + 2 fly.
+// LDS is all ring: ten slots of 256 x 32 (16 KB).  A blocked or column operand's stage is
+// one slot; W's rows, copied 64 deep, take two (the logits: six slots for W, four for the
+// hidden states; dH and dW five each).  A stage is two groups of 16 MFMAs, with one barrier
+// between them: by then the stage's last fragments are read and its slots free.  The copies
+// that follow are spread over the stage's second group and the next stage's first, one per
+// four MFMAs: issued at once by all four waves they queue at the address unit and hold up
+// the MFMAs behind them.  The barrier waits for the next stage only; two or three stages'
+// copies stay in flight (2000 to 3000 cycles; a ring of three and two 64-deep stages left
+// the second operand 1500, less than a miss takes: dW of 4096 x 8192 x 32000 1.81 ms).
 //
 // The MFMA's rows are the index that runs along the output's memory (the vocabulary for z
 // and G, the hidden width for dH and dW): a lane then holds four consecutive outputs, and
@@ -25,11 +28,10 @@
 namespace ql {
 namespace {
 
-constexpr int kT = 256;             // tile edge
-constexpr int kWideBK = 64;
-constexpr int kGroups = 256;        // workgroups: one per compute unit
-constexpr int kSlotsA = 3, kSlotsB = 2;
-constexpr int kRingElems = (kSlotsA + kSlotsB) * kT * kWideBK;
+constexpr int kT = 256;              // tile edge
+constexpr int kGroups = 256;         // workgroups: one per compute unit
+constexpr int kSlot = kT * 32;       // elements of a slot
+constexpr int kRingElems = 10 * kSlot;
 
 // Item `i` of workgroup `wg`'s list -> unit number, -1 past the end.  Workgroups go to the
 // eight XCDs in turn; each XCD takes a contiguous range of the units.
@@ -49,90 +51,115 @@ QL_DEV void tile_of(int u, int tiles_a, int tiles_b, int &ta, int &tb) {
 
 typedef f32x16 Acc[4][4];
 
-// The stream of stages: ring position and the fragments of the next group.
-template <typename OpA, typename OpB>
+// How an operand uses its part of the ring.  Stage s is 32 deep; a window is what follows
+// stage s's barrier.  PAIR false: slot s % S, and the window copies stage s + S, four copies
+// per wave.  PAIR true (64-deep copies): stages 2 P and 2 P + 1 share pair slot P % (S / 2),
+// free after stage 2 P + 1; that window and the next copy the pair S / 2 further on, four of
+// its eight copies each.
+template <typename Op, int S, bool PAIR>
+struct Lane {
+  Op op;
+  int at;               // element offset of its slots in the ring
+  int slot;             // slot (pair: first of two) of the current double stage's first stage
+
+  static QL_DEV int wrap(int s) { return s < S ? s : s - S; }
+  static QL_DEV int back(int s) { return s >= 2 ? s - 2 : s + S - 2; }
+  QL_DEV int elems(int s) const { return at + s * kSlot; }
+  // fragment t of group kk (0..3) of the current double stage, or of the next (`ahead`)
+  QL_DEV u32x4 read(const uint16_t *ring, int lane, int t, int kk, bool ahead) const {
+    if (PAIR) return op.read(ring + elems(ahead ? wrap(slot + 2) : slot), lane, t, kk);
+    return op.read(ring + elems(wrap(slot + (ahead ? 2 : 0) + (kk >> 1))), lane, t, kk & 1);
+  }
+  // copy c (0..3) of the window after stage `odd` (0, 1) of double stage d (`prev`: of the
+  // double stage before the current one); rs and rn are this item's and the next one's
+  // operand, nd this item's double stages
+  QL_DEV void copy(int base, const u32x4 &rs, const u32x4 &rn, int nd, int d, int odd, bool prev, int wv, int c) const {
+    const int cur = prev ? back(slot) : slot;
+    if (PAIR) {
+      // odd: the first half of pair d + S / 2 into this pair's slots; even: the second half
+      // of pair d - 1 + S / 2 into the slots before
+      const int P = (odd ? d : d - 1) + S / 2;
+      op.copy(P < nd ? rs : rn, base + elems(odd ? cur : back(cur)) * 2, wv, P < nd ? P : P - nd, (odd ? 0 : 4) + c);
+    } else {
+      const int s = 2 * d + odd + S;
+      op.copy(s < 2 * nd ? rs : rn, base + elems(wrap(cur + odd)) * 2, wv, s < 2 * nd ? s : s - 2 * nd, c);
+    }
+  }
+  // the copies of the windows before the first stage, but for the last one's second half
+  QL_DEV void fill(int base, const u32x4 &rs, int wv) {
+    slot = 0;
+    constexpr int units = PAIR ? S / 2 : S, each = PAIR ? 8 : 4;
+#pragma unroll
+    for (int s = 0; s < units; ++s)
+#pragma unroll
+      for (int c = 0; c < (s < units - 1 ? each : 2); ++c) op.copy(rs, base + elems(PAIR ? 2 * s : s) * 2, wv, s, c);
+  }
+};
+
+// The stream of stages: ring, operands and the fragments of the next group.
+template <typename LA, typename LB, int FLY>
 struct Stream {
-  OpA A;
-  OpB B;
+  LA A;
+  LB B;
   uint16_t *ring;
-  int base;     // its LDS address
-  int sa, sb;   // slots of the current stage
+  int base;  // its LDS address
   u32x4 fa[2][4], fb[2][4];
 
-  QL_DEV void read(int slot_a, int slot_b, int kk, int set, int f, int lane) {  // fragment f: A's, then B's
-    if (f < 4) fa[set][f] = A.read(ring + slot_a * OpA::kElems, lane, f, kk);
-    else fb[set][f - 4] = B.read(ring + kSlotsA * OpA::kElems + slot_b * OpB::kElems, lane, f - 4, kk);
+  QL_DEV void read(int kk, bool ahead, int f, int lane) {  // fragment f: A's, then B's
+    if (f < 4) fa[kk & 1][f] = A.read(ring, lane, f, kk, ahead);
+    else fb[kk & 1][f - 4] = B.read(ring, lane, f - 4, kk, ahead);
   }
-  QL_DEV void copy_a(const u32x4 &rs, int slot, int wv, int kt, int c) const {
-    A.copy(rs, base + slot * OpA::kElems * 2, wv, kt, c);
-  }
-  QL_DEV void copy_b(const u32x4 &rs, int slot, int wv, int kt, int c) const {
-    B.copy(rs, base + (kSlotsA * OpA::kElems + slot * OpB::kElems) * 2, wv, kt, c);
-  }
-  static QL_DEV int up(int s, int n, int slots) { return s + n < slots ? s + n : s + n - slots; }
-
   // this wave's copies of the next stage and its reads of this one are done; with that in
   // every wave, the next stage is whole and this one's slots are free
   static QL_DEV void sync() {
-    constexpr int kFly = OpA::kCopies;  // A's copies of the stage after the next
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt((kFly & 15) | (7 << 4) | ((kFly >> 4) << 14));  // and lgkmcnt(0)
+    __builtin_amdgcn_s_waitcnt((FLY & 15) | (7 << 4) | ((FLY >> 4) << 14));  // vmcnt(FLY) lgkmcnt(0)
     lbarrier();
     __builtin_amdgcn_sched_barrier(0);
   }
 
-  // the first item's stages 0 and 1, in the order in which the loop issues later ones
-  QL_DEV void start(const u32x4 &ra, const u32x4 &rb, int lane, int wv) {
-    sa = sb = 0;
-#pragma unroll
-    for (int c = 0; c < OpA::kCopies; ++c) copy_a(ra, 0, wv, 0, c);
-#pragma unroll
-    for (int c = 0; c < OpB::kCopies; ++c) copy_b(rb, 0, wv, 0, c);
-#pragma unroll
-    for (int c = 0; c < OpA::kCopies; ++c) copy_a(ra, 1, wv, 1, c);
-#pragma unroll
-    for (int c = 0; c < OpB::kCopies; ++c) copy_b(rb, 1, wv, 1, c);
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(((OpA::kCopies + OpB::kCopies) & 15) | (7 << 4) | (15 << 8) |
-                               (((OpA::kCopies + OpB::kCopies) >> 4) << 14));
+  QL_DEV void start(uint16_t *r, const u32x4 &ra, const u32x4 &rb, int lane, int wv) {
+    ring = r;
+    base = __builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint16_t *)r);
+    A.fill(base, ra, wv);
+    B.fill(base, rb, wv);
+    __builtin_amdgcn_s_waitcnt(0);
     lbarrier();
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int f = 0; f < 8; ++f) read(0, 0, 0, 0, f, lane);
+    for (int f = 0; f < 8; ++f) read(0, false, f, lane);
   }
 
-  // One stage: multiplies it and copies stage `kc` of the item behind ra, rb (two stages
-  // further along the stream).
-  QL_DEV void step(const u32x4 &ra, const u32x4 &rb, int kc, int lane, int wv, Acc &acc) {
-    const int sa1 = up(sa, 1, kSlotsA), sa2 = up(sa, 2, kSlotsA), sb1 = sb ^ 1;
+  // One double stage (64 deep).
+  QL_DEV void step(const u32x4 &ra, const u32x4 &na, const u32x4 &rb, const u32x4 &nb, int nd, int d, int lane, int wv,
+                   Acc &acc) {
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
-      const bool last = kk == 3;
-      const int c0 = last ? 0 : OpA::kCopies * kk / 3, c1 = last ? OpB::kCopies : OpA::kCopies * (kk + 1) / 3;
 #pragma unroll
       for (int m = 0; m < 16; ++m) {
         acc[m / 4][m % 4] = lmfma(fa[kk & 1][m / 4], fb[kk & 1][m % 4], acc[m / 4][m % 4]);
         // the next group's reads ride on this group's first half: done by its end
-        if (m < 8) read(last ? sa1 : sa, last ? sb1 : sb, last ? 0 : kk + 1, (kk + 1) & 1, m, lane);
-#pragma unroll
-        for (int c = c0 + (c1 - c0) * m / 16; c < c0 + (c1 - c0) * (m + 1) / 16; ++c) {
-          if (last) copy_b(rb, sb, wv, kc, c);
-          else copy_a(ra, sa2, wv, kc, c);
+        if (m < 8) read((kk + 1) & 3, kk == 3, m, lane);
+        // a window's first two copies of each operand follow the barrier (groups 1 and 3),
+        // the other two ride on the next stage's first group (2 and 0)
+        if (m % 4 == 3) {
+          const int c = (kk & 1 ? 0 : 2) + (m >> 3), odd = kk == 1 || kk == 2 ? 0 : 1;
+          const int dd = kk == 0 ? d - 1 : d;
+          if (m & 4) B.copy(base, rb, nb, nd, dd, odd, kk == 0, wv, c);
+          else A.copy(base, ra, na, nd, dd, odd, kk == 0, wv, c);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
-      if (kk == 2) sync();
+      if ((kk & 1) == 0) sync();
     }
-    sa = sa1;
-    sb = sb1;
+    A.slot = LA::wrap(A.slot + 2);
+    B.slot = LB::wrap(B.slot + 2);
   }
 
-  // An item of nk >= 2 stages; `na`, `nb` are the next item's operands.
-  QL_DEV void run(const u32x4 &ra, const u32x4 &rb, const u32x4 &na, const u32x4 &nb, int nk, int lane, int wv,
+  // An item of nd >= 3 double stages; na, nb: the next item's operands.
+  QL_DEV void run(const u32x4 &ra, const u32x4 &rb, const u32x4 &na, const u32x4 &nb, int nd, int lane, int wv,
                   Acc &acc) {
-    for (int kt = 0; kt < nk - 2; ++kt) step(ra, rb, kt + 2, lane, wv, acc);
-    step(na, nb, 0, lane, wv, acc);
-    step(na, nb, 1, lane, wv, acc);
+    for (int d = 0; d < nd; ++d) step(ra, na, rb, nb, nd, d, lane, wv, acc);
   }
   QL_DEV void finish() {
     __builtin_amdgcn_s_waitcnt(0);  // no copy may land after the workgroup's end
@@ -152,7 +179,7 @@ QL_DEV u32x4 eight(const float (&a)[4], const float (&b)[4]) {
 
 }  // namespace
 
-// GRAD false: part[64 K-row half of a tile][token] = (max, sum of exp(z - max)) over 128
+// GRAD false: part[half of a tile][token] = (max, sum of exp(z - max)) over 128
 // vocabulary rows, and zlab of the tokens whose label is among them.
 // GRAD true: G[token][v] = bf16((exp(z - lse) - [v is the label]) * (dloss / top)).
 template <bool GRAD>
@@ -165,58 +192,56 @@ __global__ __launch_bounds__(kThreads) void head_logits_wide_kernel(LogitParams 
   int u = unit_of(wg, 0, units);
   if (u < 0) return;
   const int wa = (wv >> 1) * 128, wb = (wv & 1) * 128;
-  Stream<RowOperand<kT, kWideBK>, RowOperand<kT, kWideBK>> S;
-  S.ring = ring;
-  S.base = __builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint16_t *)ring);
-  S.A.init(p.h, lane, wv, wa);
-  S.B.init(p.h, lane, wv, wb);
+  // W's pairs of slots: three; the hidden states' slots: four.  At a barrier the copies of
+  // two windows may be in flight.
+  Stream<Lane<RowOperand<kT, 64>, 6, true>, Lane<BlockRows<kT, 32>, 4, false>, 16> S;
+  S.A.op.init(p.h, lane, wv, wa);
+  S.B.op.init(p.h * 64, lane, wv, wb);
+  S.A.at = 0, S.B.at = 6 * kSlot;
   auto operands = [&](int unit, u32x4 &ra, u32x4 &rb) {
     int tv, tt;
     tile_of(unit, p.tiles_v, tiles_t, tv, tt);
     ra = lrsrc(p.W + (int64_t)tv * kT * p.h, (p.nvoc - (int64_t)tv * kT) * p.h * 2);
-    rb = lrsrc(p.H + (int64_t)tt * kT * p.h, ((int64_t)n - (int64_t)tt * kT) * p.h * 2);
+    rb = lrsrc(p.H + (int64_t)tt * kT * p.h, ((n + 31) / 32 * 32 - (int64_t)tt * kT) * p.h * 2);
   };
   u32x4 ra, rb, na, nb;
   operands(u, ra, rb);
-  S.start(ra, rb, lane, wv);
-  const int nk = (int)(p.h / kWideBK);
+  S.start(ring, ra, rb, lane, wv);
+  const int nd = (int)(p.h / 64);
   const float top = GRAD ? *p.top : 0.0f;
   for (int i = 1; u >= 0; ++i) {
     const int next = unit_of(wg, i, units);
     operands(next >= 0 ? next : u, na, nb);
     Acc acc;
     clear(acc);
-    S.run(ra, rb, na, nb, nk, lane, wv, acc);
+    S.run(ra, rb, na, nb, nd, lane, wv, acc);
     int tv, tt;
     tile_of(u, p.tiles_v, tiles_t, tv, tt);
     const int64_t v0 = (int64_t)tv * kT, t0 = (int64_t)tt * kT;
-    const int rows = (int)(p.nvoc - v0 < kT ? p.nvoc - v0 : kT) - wa;  // vocabulary rows of this wave's 128
+    // A lane holds rows 4 g + c of the wave's 128, c = 32 ii + 8 q + e known at compile time:
+    // rows and labels are taken relative to 4 g, so that only c is compared with.
+    const int lim = (int)(p.nvoc - v0 < kT ? p.nvoc - v0 : kT) - wa - 4 * g;  // rows of the vocabulary: c < lim
+    const int vbase = (int)(p.v0 + v0) + wa + 4 * g;
     if constexpr (!GRAD) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int64_t t = t0 + wb + 32 * j + l32;
-        // the label's place among this wave's rows (outside [0, 128): not here)
-        const int64_t lab = t < n ? (int64_t)p.label[t] - p.v0 - v0 - wa : -1;
-        if (__any(lab >= 0 && lab < 128)) {
+        const int lab = t < n ? p.label[t] - vbase : -1;
+        const bool mine = lab >= 0 && lab < 128 && !(lab & 4);  // (bit 2 set: the other half's)
+        if (__any(mine)) {
           float z = 0.0f;
-          const int l = (int)lab - 4 * g;  // rows 32 i + 8 q + e of the lane's half
-          bool mine = false;
 #pragma unroll
           for (int ii = 0; ii < 4; ++ii)
 #pragma unroll
-            for (int v = 0; v < 16; ++v) {
-              const bool hit = l == 32 * ii + acc_row(v, 0) && lab >= 0 && lab < 128;
-              z = hit ? acc[ii][j][v] : z;
-              mine |= hit;
-            }
+            for (int v = 0; v < 16; ++v) z = lab == 32 * ii + acc_row(v, 0) ? acc[ii][j][v] : z;
           if (mine) p.zlab[t] = z;
         }
-        if (rows < 128) {
+        if (__any(lim < 128 - 4 * g)) {
 #pragma unroll
           for (int ii = 0; ii < 4; ++ii)
 #pragma unroll
             for (int v = 0; v < 16; ++v)
-              if (32 * ii + acc_row(v, g) >= rows) acc[ii][j][v] = -__builtin_inff();
+              if (32 * ii + acc_row(v, 0) >= lim) acc[ii][j][v] = -__builtin_inff();
         }
         float mx = -__builtin_inff();
 #pragma unroll
@@ -239,8 +264,10 @@ __global__ __launch_bounds__(kThreads) void head_logits_wide_kernel(LogitParams 
         const int64_t t = t0 + wb + 32 * j + l32;
         const bool live = t < n;
         const float lse = live ? p.lse[t] : 0.0f, dl = live && top > 0.0f ? p.dloss[t] / top : 0.0f;
-        const int64_t lab = live ? (int64_t)p.label[t] - p.v0 - v0 - wa : -1;
-        uint16_t *dst = p.G + t * p.ldg + v0 + wa + 8 * g;
+        const int lab = live ? p.label[t] - vbase : -1;
+        // blocks of G: the wave's 32 tokens are one block row, tile ii one block (tokens past
+        // the last: zero; the tile's rows are all there)
+        uint16_t *dst = p.G + blocked(t, v0 + wa, p.gblocks) + 8 * g;
 #pragma unroll
         for (int ii = 0; ii < 4; ++ii)
 #pragma unroll
@@ -250,12 +277,11 @@ __global__ __launch_bounds__(kThreads) void head_logits_wide_kernel(LogitParams 
             for (int q = 0; q < 2; ++q)
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const int row = 32 * ii + 16 * pp + 8 * q + 4 * g + e;
+                const int c = 32 * ii + 16 * pp + 8 * q + e;
                 const float pr = __expf(acc[ii][j][8 * pp + 4 * q + e] - lse);
-                o[q][e] = row < rows ? (row == lab ? pr - 1.0f : pr) * dl : 0.0f;
+                o[q][e] = c < lim ? (c == lab ? pr - 1.0f : pr) * dl : 0.0f;
               }
-            const u32x4 w = eight(o[0], o[1]);  // every lane: the swap needs both halves
-            if (live) *reinterpret_cast<u32x4 *>(dst + 32 * ii + 16 * pp) = w;
+            *reinterpret_cast<u32x4 *>(dst + 1024 * ii + 16 * pp) = eight(o[0], o[1]);
           }
       }
     }
@@ -279,15 +305,15 @@ __global__ __launch_bounds__(kThreads) void head_dh_wide_kernel(HeadGradParams p
   int u = unit_of(wg, 0, units);
   if (u < 0) return;
   const int wa = (wv >> 1) * 128, wb = (wv & 1) * 128;
-  Stream<ColOperand<kT, kWideBK>, RowOperand<kT, kWideBK>> S;
-  S.ring = ring;
-  S.base = __builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint16_t *)ring);
-  S.A.init(p.h, lane, wv, wa);
-  S.B.init(p.ldg, lane, wv, wb);
+  Stream<Lane<ColOperand<kT, 32>, 5, false>, Lane<BlockRows<kT, 32>, 5, false>, 24> S;
+  S.A.op.init(p.h, lane, wv, wa);
+  S.B.op.init(p.gblocks * 2048, lane, wv, wb);
+  S.A.at = 0, S.B.at = 5 * kSlot;
   const int64_t seg = col_segment(p.h) / 64;  // blocks of 64 entries within 32-bit offsets
-  // A unit's blocks [b0, b1) from block `from`: the operands and the number of stages.  W's
-  // rows from the range's end on read as zero, so two stages are always right.
-  auto operands = [&](int unit, int64_t from, u32x4 &ra, u32x4 &rb, int &nk, int64_t &to) {
+  // A unit's blocks [b0, b1) of 64 entries from block `from`: the operands and the number of
+  // double stages.  W's rows from the range's end on read as zero, so three are always
+  // right (G's columns there are written, or past its end).
+  auto operands = [&](int unit, int64_t from, u32x4 &ra, u32x4 &rb, int &nd, int64_t &to) {
     int th, tt;
     tile_of(unit % tiles, tiles_h, tiles_t, th, tt);
     const int s = unit / tiles;
@@ -295,22 +321,28 @@ __global__ __launch_bounds__(kThreads) void head_dh_wide_kernel(HeadGradParams p
     const int64_t b = from < 0 ? b0 : from, e = b1 - b < seg ? b1 : b + seg;
     const int64_t k1 = e * 64 < p.nvoc ? e * 64 : p.nvoc;
     ra = lrsrc(p.W + b * 64 * p.h + (int64_t)th * kT, (k1 - b * 64) * p.h * 2 - (int64_t)th * kT * 2);
-    rb = lrsrc(p.G + (int64_t)tt * kT * p.ldg + b * 64, ((int64_t)n - (int64_t)tt * kT) * p.ldg * 2 - b * 128);
-    nk = (int)(e - b > 2 ? e - b : 2);
+    const int64_t at = (int64_t)tt * (kT / 32) * p.gblocks + 2 * b;  // in blocks of 2 KB
+    rb = lrsrc(p.G + at * 1024, ((n + 31) / 32 * p.gblocks - at) * 2048);
+    nd = (int)(e - b > 3 ? e - b : 3);
     to = e < b1 ? e : -1;  // the unit goes on at block e
   };
   u32x4 ra, rb, na, nb;
-  int nk, nkn;
+  int nd, ndn;
   int64_t to, ton;
-  operands(u, -1, ra, rb, nk, to);
-  S.start(ra, rb, lane, wv);
-  Acc acc;
-  clear(acc);
-  for (int i = 1; u >= 0;) {
-    const int next = to >= 0 ? u : unit_of(wg, i, units);
-    operands(next >= 0 ? next : u, to, na, nb, nkn, ton);
-    S.run(ra, rb, na, nb, nk, lane, wv, acc);
-    if (to < 0) {
+  operands(u, -1, ra, rb, nd, to);
+  S.start(ring, ra, rb, lane, wv);
+  for (int i = 1; u >= 0; ++i) {
+    Acc acc;
+    clear(acc);
+    for (;;) {  // the unit's segments
+      const int next = to >= 0 ? u : unit_of(wg, i, units);
+      operands(next >= 0 ? next : u, to, na, nb, ndn, ton);
+      S.run(ra, rb, na, nb, nd, lane, wv, acc);
+      const bool more = to >= 0;
+      ra = na, rb = nb, nd = ndn, to = ton;
+      if (!more) break;
+    }
+    {
       int th, tt;
       tile_of(u % tiles, tiles_h, tiles_t, th, tt);
       float *out = p.part + (int64_t)(u / tiles) * n * p.h;
@@ -329,11 +361,8 @@ __global__ __launch_bounds__(kThreads) void head_dh_wide_kernel(HeadGradParams p
             *reinterpret_cast<f32x4 *>(dst + c) = v;
           }
       }
-      clear(acc);
-      ++i;
     }
-    u = next;
-    ra = na, rb = nb, nk = nkn, to = ton;
+    u = unit_of(wg, i, units);
   }
   S.finish();
 }
@@ -349,36 +378,43 @@ __global__ __launch_bounds__(kThreads) void head_dw_wide_kernel(HeadGradParams p
   int u = unit_of(wg, 0, units);
   if (u < 0) return;
   const int wa = (wv >> 1) * 128, wb = (wv & 1) * 128;
-  Stream<ColOperand<kT, kWideBK>, ColOperand<kT, kWideBK>> S;
-  S.ring = ring;
-  S.base = __builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint16_t *)ring);
-  S.A.init(p.h, lane, wv, wa);
-  S.B.init(p.ldg, lane, wv, wb);
-  const int blocks = (n + 63) / 64;
-  const int64_t seg = col_segment(p.h > p.ldg ? p.h : p.ldg) / 64;
-  // both operands read as zero from token n on
-  auto operands = [&](int unit, int64_t from, u32x4 &ra, u32x4 &rb, int &nk, int64_t &to) {
+  Stream<Lane<BlockCols<kT>, 5, false>, Lane<BlockCols<kT>, 5, false>, 24> S;
+  S.A.op.init(p.h * 64, lane, wv, wa);
+  S.B.op.init(p.gblocks * 2048, lane, wv, wb);
+  S.A.at = 0, S.B.at = 5 * kSlot;
+  const int blocks = (n + 63) / 64, rows32 = (n + 31) / 32;
+  // 64-token steps within 32-bit offsets, the copies past the end included
+  const int64_t wide = p.h * 64 > p.gblocks * 2048 ? p.h * 64 : p.gblocks * 2048;
+  const int64_t seg = (((int64_t)1 << 31) - 65536) / (2 * wide) - 4;
+  // both operands are zero from token n to the next 32 and read as zero from there on
+  auto operands = [&](int unit, int64_t from, u32x4 &ra, u32x4 &rb, int &nd, int64_t &to) {
     int th, tv;
     tile_of(unit, tiles_h, tiles_v, th, tv);
-    const int64_t b = from < 0 ? 0 : from, e = blocks - b < seg ? blocks : b + seg, t = b * 64;
-    ra = lrsrc(p.H + t * p.h + (int64_t)th * kT, (n - t) * p.h * 2 - (int64_t)th * kT * 2);
-    rb = lrsrc(p.G + t * p.ldg + (int64_t)tv * kT, (n - t) * p.ldg * 2 - (int64_t)tv * kT * 2);
-    nk = (int)(e - b > 2 ? e - b : 2);
+    const int64_t b = from < 0 ? 0 : from, e = blocks - b < seg ? blocks : b + seg;
+    const int64_t ha = 2 * b * (p.h / 32) + th * (kT / 32), ga = 2 * b * p.gblocks + tv * (kT / 32);  // in blocks
+    ra = lrsrc(p.H + ha * 1024, (rows32 * (p.h / 32) - ha) * 2048);
+    rb = lrsrc(p.G + ga * 1024, (rows32 * p.gblocks - ga) * 2048);
+    nd = (int)(e - b > 3 ? e - b : 3);
     to = e < blocks ? e : -1;
   };
   u32x4 ra, rb, na, nb;
-  int nk, nkn;
+  int nd, ndn;
   int64_t to, ton;
-  operands(u, -1, ra, rb, nk, to);
-  S.start(ra, rb, lane, wv);
+  operands(u, -1, ra, rb, nd, to);
+  S.start(ring, ra, rb, lane, wv);
   const float top = n > 0 ? *p.top : 0.0f;
-  Acc acc;
-  clear(acc);
-  for (int i = 1; u >= 0;) {
-    const int next = to >= 0 ? u : unit_of(wg, i, units);
-    operands(next >= 0 ? next : u, to, na, nb, nkn, ton);
-    S.run(ra, rb, na, nb, nk, lane, wv, acc);
-    if (to < 0) {
+  for (int i = 1; u >= 0; ++i) {
+    Acc acc;
+    clear(acc);
+    for (;;) {  // the unit's segments
+      const int next = to >= 0 ? u : unit_of(wg, i, units);
+      operands(next >= 0 ? next : u, to, na, nb, ndn, ton);
+      S.run(ra, rb, na, nb, nd, lane, wv, acc);
+      const bool more = to >= 0;
+      ra = na, rb = nb, nd = ndn, to = ton;
+      if (!more) break;
+    }
+    {
       int th, tv;
       tile_of(u, tiles_h, tiles_v, th, tv);
 #pragma unroll
@@ -399,11 +435,8 @@ __global__ __launch_bounds__(kThreads) void head_dw_wide_kernel(HeadGradParams p
             if (v < p.nvoc && c < p.h) *reinterpret_cast<u32x4 *>(dst + c) = w;
           }
       }
-      clear(acc);
-      ++i;
     }
-    u = next;
-    ra = na, rb = nb, nk = nkn, to = ton;
+    u = unit_of(wg, i, units);
   }
   S.finish();
 }
