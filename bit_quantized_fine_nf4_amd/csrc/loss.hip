@@ -201,8 +201,8 @@ int few_splits(int64_t h, int64_t piece) {
   return (int)(s < 1 ? 1 : s);
 }
 
-// Rows of partial sums: every token once, and room to split few tokens' sums.
-int64_t partial_rows(int64_t M) { return M > 4096 ? M : (16 * M < 4096 ? 16 * M : 4096); }
+// Rows of partial sums: every token once, and room to split the sums of up to 8192.
+int64_t partial_rows(int64_t M) { return M > 8192 ? M : (16 * M < 8192 ? 16 * M : 8192); }
 
 struct LossLayout {
   size_t count, top, idx, label, lse, dloss, hc, stat, zlab, g, part, total;
