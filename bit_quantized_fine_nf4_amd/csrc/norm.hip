@@ -117,48 +117,97 @@ QL_DEV void store8(float *p, const float (&x)[8], int n) {
   }
 }
 
-// Sum over the workgroup of B threads, in a fixed order; `red` has B / 64 floats that
+// Sum over a wave, the same for every lane: quads, halves and rows of 16 by DPP, then lane
+// 15 of a row into the next row and lane 31 into the upper half; lane 63 has the total.
+QL_DEV float wave_sum(float v) {
+#define QL_DPP(ctrl, rows) \
+  __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), ctrl, rows, 0xF, false))
+  v += QL_DPP(0xB1, 0xF);   // quad_perm [1,0,3,2]
+  v += QL_DPP(0x4E, 0xF);   // quad_perm [2,3,0,1]
+  v += QL_DPP(0x141, 0xF);  // row_half_mirror
+  v += QL_DPP(0x140, 0xF);  // row_mirror
+  v += QL_DPP(0x142, 0xA);  // row_bcast:15
+  v += QL_DPP(0x143, 0xC);  // row_bcast:31
+#undef QL_DPP
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
+
+constexpr int kMaxWaves = 16;
+
+// Sum over the workgroup's nw waves, in a fixed order; `red` has a float per wave that
 // nobody reads or writes until the barrier of the call after the next one.
-template <int B>
-QL_DEV float wg_sum(float v, float *red) {
+QL_DEV float wg_sum(float v, float *red, int nw) {
+  v = wave_sum(v);
+  if (nw == 1) return v;
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = red[0];
 #pragma unroll
-  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m, 64);
-  if constexpr (B > 64) {
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = red[0];
-#pragma unroll
-    for (int w = 1; w < B / 64; ++w) v += red[w];
-  }
+  for (int w = 1; w < kMaxWaves; ++w)
+    if (w < nw) v += red[w];
   return v;
 }
 
 }  // namespace
 
-// B threads per row, NV pieces of eight values per thread (8 B NV >= h).
-template <typename RT, int B, int NV, bool TAIL>
-__global__ __launch_bounds__(B) void norm_fwd_kernel(NormFwdArgs p) {
-  __shared__ float red[4][B / 64];
-  const int tid = threadIdx.x;
+// Eight weights; ones where there are none (a product with 1 changes nothing).
+template <bool TAIL>
+QL_DEV Piece<float> weights(const float *w, int c, int h) {
+  Piece<float> p;
+  if (w) {
+    p.load<TAIL>(w + (c < h ? c : 0), c < h ? h - c : 0);
+  } else {
+    p.a = f32x4{1, 1, 1, 1};
+    p.b = f32x4{1, 1, 1, 1};
+  }
+  return p;
+}
+
+// NV pieces of eight values per thread, whole waves (8 NV blockDim >= h).  A workgroup walks
+// the rows blockIdx.x, + gridDim.x, ...: its weights stay in registers (alpha * gate *
+// w_post as one), and the next row is loaded before this one's sums, whose barriers would
+// otherwise leave the memory idle.
+template <typename RT, int NV, bool TAIL>
+__global__ __launch_bounds__(1024) void norm_fwd_kernel(NormFwdArgs p) {
+  __shared__ float red[4][kMaxWaves];
+  const int tid = threadIdx.x, B = blockDim.x, nw = B >> 6;
   const int h = (int)p.h;
   const RT *R = reinterpret_cast<const RT *>(p.R);
   RT *Ro = reinterpret_cast<RT *>(p.R_out);
   const float inv_h = 1.0f / (float)h;
-  int slot = 0;
-  for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
-    float r[NV][8];
-    Piece<RT> rr[NV];
-    Piece<uint16_t> yy[NV];
+  Piece<float> wp[NV];
+  float a[NV][8];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = 8 * (tid + B * j);
+    const Piece<float> wq = weights<TAIL>(p.w_post, c, h), wg = weights<TAIL>(p.gate, c, h);
+    wp[j] = weights<TAIL>(p.w_pre, c, h);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[j][i] = p.alpha * wg.get(i) * wq.get(i);
+  }
+  Piece<RT> rr[NV];
+  Piece<uint16_t> yy[NV];
+  auto load = [&](int64_t m) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = 8 * (tid + B * j);
-      rr[j].template load<TAIL>(R + m * h + (c < h ? c : 0), c < h ? h - c : 0);
-      if (p.Y) yy[j].template load<TAIL>(p.Y + m * h + (c < h ? c : 0), c < h ? h - c : 0);
+      const int c = 8 * (tid + B * j), n = m < p.M && c < h ? h - c : 0;
+      const int64_t at = n ? m * h + c : 0;
+      rr[j].template load<TAIL>(R + at, n);
+      yy[j].template load<TAIL>(p.Y + at, p.Y ? n : 0);
     }
+  };
+  load(blockIdx.x);
+  int slot = 0;
+  for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
+    float r[NV][8], u[NV][8];
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) r[j][i] = rr[j].get(i);
+      for (int i = 0; i < 8; ++i) {
+        r[j][i] = rr[j].get(i);
+        u[j][i] = yy[j].get(i);
+      }
+    load(m + gridDim.x);
     if (p.Y) {
       float rs = 1.0f;
       if (p.w_post) {
@@ -166,33 +215,16 @@ __global__ __launch_bounds__(B) void norm_fwd_kernel(NormFwdArgs p) {
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(yy[j].get(i), yy[j].get(i), ss);
-        rs = 1.0f / sqrtf(wg_sum<B>(ss, red[slot]) * inv_h + p.eps);
+          for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(u[j][i], u[j][i], ss);
+        rs = 1.0f / sqrtf(wg_sum(ss, red[slot], nw) * inv_h + p.eps);
         slot = (slot + 1) & 3;
         if (p.rstd_post && tid == 0) p.rstd_post[m] = rs;
       }
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int c = 8 * (tid + B * j);
-        if (c >= h) continue;
-        Piece<float> w, g;
-        if (p.w_post) w.template load<TAIL>(p.w_post + c, h - c);
-        if (p.gate) g.template load<TAIL>(p.gate + c, h - c);
-        float o[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float u = yy[j].get(i);
-          if (p.w_post) u = u * rs * w.get(i);
-          const float a = p.gate ? p.alpha * g.get(i) : p.alpha;
-          r[j][i] = __builtin_fmaf(a, u, r[j][i]);
-          o[i] = r[j][i];
-        }
-        store8<TAIL>(Ro + m * h + c, o, h - c);
-      }
-    } else if (Ro) {
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int c = 8 * (tid + B * j);
+        for (int i = 0; i < 8; ++i) r[j][i] = __builtin_fmaf(a[j][i], u[j][i] * rs, r[j][i]);
         if (c < h) store8<TAIL>(Ro + m * h + c, r[j], h - c);
       }
     }
@@ -202,140 +234,127 @@ __global__ __launch_bounds__(B) void norm_fwd_kernel(NormFwdArgs p) {
       for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(r[j][i], r[j][i], ss);
-      const float rs = 1.0f / sqrtf(wg_sum<B>(ss, red[slot]) * inv_h + p.eps);
+      const float rs = 1.0f / sqrtf(wg_sum(ss, red[slot], nw) * inv_h + p.eps);
       slot = (slot + 1) & 3;
       if (p.rstd_pre && tid == 0) p.rstd_pre[m] = rs;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int c = 8 * (tid + B * j);
-        if (c >= h) continue;
-        Piece<float> w;
-        w.template load<TAIL>(p.w_pre + c, h - c);
         float o[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = r[j][i] * rs * w.get(i);
-        store8<TAIL>(p.N + m * h + c, o, h - c);
+        for (int i = 0; i < 8; ++i) o[i] = r[j][i] * rs * wp[j].get(i);
+        if (c < h) store8<TAIL>(p.N + m * h + c, o, h - c);
       }
     }
   }
 }
 
-// Backward.  A workgroup takes the rows blockIdx.x, + gridDim.x, ...; with SUMS it
-// keeps its rows' contributions to the three weight gradients in registers and
-// stores them once, as row blockIdx.x of part[3][gridDim.x][h] (norm_sum_kernel adds
-// the rows in a fixed order: no atomics, the same bits every time).
-template <typename RT, int B, int NV, bool SUMS, bool TAIL>
-__global__ __launch_bounds__(B) void norm_bwd_kernel(NormBwdArgs p, float *__restrict__ part) {
-  __shared__ float red[4][B / 64];
-  const int tid = threadIdx.x;
+// Backward, rows as above.  The weights' gradients are sums over rows of two products only,
+// dN * x and dR * y: w_post's and gate's are constants of the column times the second.  With
+// SUMS a workgroup keeps its rows' sums in registers and stores them once, as row blockIdx.x
+// of part[2][gridDim.x][h] (norm_sum_kernel adds the rows in a fixed order: no atomics, the
+// same bits every time).  The next row is loaded before this one's sums where one piece per
+// thread holds a row (h <= 8192); wider rows have no registers left for it.
+template <typename RT, int NV, bool SUMS, bool TAIL>
+__global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs p, float *__restrict__ part) {
+  constexpr bool AHEAD = NV == 1;
+  __shared__ float red[4][kMaxWaves];
+  const int tid = threadIdx.x, B = blockDim.x, nw = B >> 6;
   const int h = (int)p.h;
   const RT *Ro = reinterpret_cast<const RT *>(p.R_out), *dRo = reinterpret_cast<const RT *>(p.dR_out);
   RT *dR = reinterpret_cast<RT *>(p.dR);
   const float inv_h = 1.0f / (float)h;
   constexpr int NS = SUMS ? NV : 1;
-  float s_pre[NS][8], s_post[NS][8], s_gate[NS][8];
+  float s_pre[NS][8], s_y[NS][8];
 #pragma unroll
   for (int j = 0; j < NS; ++j)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s_pre[j][i] = s_post[j][i] = s_gate[j][i] = 0.0f;
-  int slot = 0;
-  for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
-    Piece<uint16_t> dn[NV], yy[NV];
-    Piece<RT> ro[NV], dro[NV];
+    for (int i = 0; i < 8; ++i) s_pre[j][i] = s_y[j][i] = 0.0f;
+  Piece<float> wp[NV];
+  float a[NV][8];  // alpha * gate * w_post
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = 8 * (tid + B * j);
+    const Piece<float> wq = weights<TAIL>(p.w_post, c, h), wg = weights<TAIL>(p.gate, c, h);
+    wp[j] = weights<TAIL>(p.w_pre, c, h);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[j][i] = p.alpha * wg.get(i) * wq.get(i);
+  }
+  Piece<uint16_t> dn[NV], yy[NV];
+  Piece<RT> ro[NV], dro[NV];
+  float rsp = 0.0f, rsq = 1.0f;
+  auto load = [&](int64_t m) {
+    const bool in = m < p.M;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = 8 * (tid + B * j), n = c < h ? h - c : 0;
-      const int64_t at = m * h + (n ? c : 0);
-      dn[j].template load<TAIL>(p.dN ? p.dN + at : nullptr, p.dN ? n : 0);
-      ro[j].template load<TAIL>(p.w_pre ? Ro + at : nullptr, p.w_pre ? n : 0);
-      dro[j].template load<TAIL>(dRo ? dRo + at : nullptr, dRo ? n : 0);
-      yy[j].template load<TAIL>(p.Y ? p.Y + at : nullptr, p.Y ? n : 0);
+      const int c = 8 * (tid + B * j), n = in && c < h ? h - c : 0;
+      const int64_t at = n ? m * h + c : 0;
+      dn[j].template load<TAIL>(p.dN + at, p.dN ? n : 0);
+      ro[j].template load<TAIL>(Ro + at, p.w_pre ? n : 0);
+      dro[j].template load<TAIL>(dRo + at, dRo ? n : 0);
+      yy[j].template load<TAIL>(p.Y + at, p.Y ? n : 0);
     }
-    float dr[NV][8];
-    if (p.w_pre) {
-      const float rs = p.rstd_pre[m];
-      float dot = 0.0f;
+    rsp = in && p.w_pre ? p.rstd_pre[m] : 0.0f;
+    rsq = in && p.w_post ? p.rstd_post[m] : 1.0f;
+  };
+  load(blockIdx.x);
+  int slot = 0;
+  for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
+    float d[NV][8], x[NV][8], y[NV][8], dr[NV][8];
+    const float rp = rsp, rq = rsq;
+    float dot = 0.0f;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int c = 8 * (tid + B * j);
-        Piece<float> w;
-        w.template load<TAIL>(p.w_pre + (c < h ? c : 0), c < h ? h - c : 0);
+    for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float x = ro[j].get(i) * rs, d = dn[j].get(i) * w.get(i);
-          dr[j][i] = d;
-          dot = __builtin_fmaf(d, x, dot);
-          if (SUMS) s_pre[SUMS ? j : 0][i] = __builtin_fmaf(dn[j].get(i), x, s_pre[SUMS ? j : 0][i]);
-        }
+      for (int i = 0; i < 8; ++i) {
+        const float g = dn[j].get(i);
+        x[j][i] = ro[j].get(i) * rp;
+        y[j][i] = yy[j].get(i) * rq;
+        d[j][i] = g * wp[j].get(i);
+        dr[j][i] = dro[j].get(i);
+        dot = __builtin_fmaf(d[j][i], x[j][i], dot);
+        if (SUMS) s_pre[SUMS ? j : 0][i] = __builtin_fmaf(g, x[j][i], s_pre[SUMS ? j : 0][i]);
       }
-      dot = wg_sum<B>(dot, red[slot]) * inv_h;
+    if (AHEAD) load(m + gridDim.x);
+    if (p.w_pre) {
+      dot = wg_sum(dot, red[slot], nw) * inv_h;
       slot = (slot + 1) & 3;
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          dr[j][i] = dro[j].get(i) + rs * (dr[j][i] - ro[j].get(i) * rs * dot);
-    } else {
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) dr[j][i] = dro[j].get(i);
+        for (int i = 0; i < 8; ++i) dr[j][i] += rp * (d[j][i] - x[j][i] * dot);
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = 8 * (tid + B * j);
       if (c < h) store8<TAIL>(dR + m * h + c, dr[j], h - c);
     }
-    if (!p.dY) continue;
-    if (p.w_post) {
-      const float rs = p.rstd_post[m];
-      float dot = 0.0f;
+    if (p.dY) {
+      dot = 0.0f;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int c = 8 * (tid + B * j), n = c < h ? h - c : 0;
-        Piece<float> w, g;
-        w.template load<TAIL>(p.w_post + (n ? c : 0), n);
-        if (p.gate) g.template load<TAIL>(p.gate + (n ? c : 0), n);
+      for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float y = yy[j].get(i) * rs;
-          const float adr = p.alpha * dr[j][i], du = p.gate ? adr * g.get(i) : adr, d = du * w.get(i);
-          if (SUMS) {
-            s_post[SUMS ? j : 0][i] = __builtin_fmaf(du, y, s_post[SUMS ? j : 0][i]);
-            s_gate[SUMS ? j : 0][i] = __builtin_fmaf(adr, y * w.get(i), s_gate[SUMS ? j : 0][i]);
-          }
-          dot = __builtin_fmaf(d, y, dot);
-          dr[j][i] = d;
+          // without a norm after the block y is Y, and the gradient ends here
+          if (SUMS) s_y[SUMS ? j : 0][i] = __builtin_fmaf(dr[j][i], y[j][i], s_y[SUMS ? j : 0][i]);
+          dr[j][i] *= a[j][i];
+          dot = __builtin_fmaf(dr[j][i], y[j][i], dot);
         }
+      if (p.w_post) {
+        dot = wg_sum(dot, red[slot], nw) * inv_h;
+        slot = (slot + 1) & 3;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dr[j][i] = rq * (dr[j][i] - y[j][i] * dot);
       }
-      dot = wg_sum<B>(dot, red[slot]) * inv_h;
-      slot = (slot + 1) & 3;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int c = 8 * (tid + B * j);
-        if (c >= h) continue;
-        float o[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = rs * (dr[j][i] - yy[j].get(i) * rs * dot);
-        store8<TAIL>(p.dY + m * h + c, o, h - c);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int c = 8 * (tid + B * j);
-        if (c >= h) continue;
-        Piece<float> g;
-        if (p.gate) g.template load<TAIL>(p.gate + c, h - c);
-        float o[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float adr = p.alpha * dr[j][i];
-          o[i] = p.gate ? adr * g.get(i) : adr;
-          if (SUMS) s_gate[SUMS ? j : 0][i] = __builtin_fmaf(adr, yy[j].get(i), s_gate[SUMS ? j : 0][i]);
-        }
-        store8<TAIL>(p.dY + m * h + c, o, h - c);
+        if (c < h) store8<TAIL>(p.dY + m * h + c, dr[j], h - c);
       }
     }
+    if (!AHEAD) load(m + gridDim.x);
   }
   if constexpr (SUMS) {
     const int64_t plane = (int64_t)gridDim.x * h;
@@ -345,30 +364,28 @@ __global__ __launch_bounds__(B) void norm_bwd_kernel(NormBwdArgs p, float *__res
       const int c = 8 * (tid + B * j);
       if (c >= h) continue;
       if (p.dw_pre) store8<TAIL>(out + c, s_pre[j], h - c);
-      if (p.dw_post) store8<TAIL>(out + plane + c, s_post[j], h - c);
-      if (p.dgate) store8<TAIL>(out + 2 * plane + c, s_gate[j], h - c);
+      if (p.dw_post || p.dgate) store8<TAIL>(out + plane + c, s_y[j], h - c);
     }
   }
 }
 
-// out[k][c] = sum of the `rows` partial rows of weight gradient k = blockIdx.y.  A
-// workgroup takes 64 columns; its 16 waves take the rows w, w + 16, ... and are added
-// in wave order.
-__global__ __launch_bounds__(1024) void norm_sum_kernel(const float *__restrict__ part, int rows, int64_t h,
-                                                        float *dw_pre, float *dw_post, float *dgate) {
+// Weight gradients from the `rows` partial rows: plane 0 is dw_pre; plane 1, S = sum dR * y,
+// gives dw_post = alpha * gate * S and dgate = alpha * w_post * S.  A workgroup takes 64
+// columns of a plane; its 16 waves take the rows w, w + 16, ... and are added in wave order.
+__global__ __launch_bounds__(1024) void norm_sum_kernel(const float *__restrict__ part, int rows, NormBwdArgs p) {
   __shared__ float red[16][64];
-  float *out = blockIdx.y == 0 ? dw_pre : (blockIdx.y == 1 ? dw_post : dgate);
-  if (!out) return;  // the whole workgroup
+  if (blockIdx.y == 0 ? !p.dw_pre : !(p.dw_post || p.dgate)) return;  // the whole workgroup
   const int l = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int64_t c = (int64_t)blockIdx.x * 64 + l;
+  const int64_t h = p.h, c = (int64_t)blockIdx.x * 64 + l;
   const float *src = part + (int64_t)blockIdx.y * rows * h + c;
   float s = 0.0f;
   if (c < h) {
     int k = w;
-    for (; k + 48 < rows; k += 64) {
-      const float a = src[(int64_t)k * h], b = src[(int64_t)(k + 16) * h];
-      const float d = src[(int64_t)(k + 32) * h], e = src[(int64_t)(k + 48) * h];
-      s += (a + b) + (d + e);
+    for (; k + 112 < rows; k += 128) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = src[(int64_t)(k + 16 * i) * h];
+      s += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
     }
     for (; k < rows; k += 16) s += src[(int64_t)k * h];
   }
@@ -377,39 +394,41 @@ __global__ __launch_bounds__(1024) void norm_sum_kernel(const float *__restrict_
   if (w == 0 && c < h) {
 #pragma unroll
     for (int i = 1; i < 16; ++i) s += red[i][l];
-    out[c] = s;
+    if (blockIdx.y == 0) {
+      p.dw_pre[c] = s;
+    } else {
+      if (p.dw_post) p.dw_post[c] = p.alpha * (p.gate ? p.gate[c] : 1.0f) * s;
+      if (p.dgate) p.dgate[c] = p.alpha * (p.w_post ? p.w_post[c] : 1.0f) * s;
+    }
   }
 }
 
 namespace {
 
-// Rows of partial sums: one workgroup per compute unit for rows of 1024 threads and
-// proportionally more of the smaller ones.
-int bwd_grid(int64_t M, int64_t h) {
-  const int64_t per = h <= 2048 ? 1024 : (h <= 4096 ? 512 : 256);
+// Threads per row: one piece each up to 8192 values, two beyond, in whole waves.
+int row_threads(int64_t h) {
+  const int64_t v = (h + 7) / 8, t = v <= 1024 ? v : (v + 1) / 2;
+  return (int)((t + 63) / 64 * 64);
+}
+// Workgroups for M rows: `threads` per compute unit.
+int rows_grid(int64_t M, int64_t h, int threads) {
+  const int64_t per = 256 * (int64_t)(threads / row_threads(h));
   return (int)(M < per ? M : per);
 }
+constexpr int kFwdThreads = 2048, kBwdThreads = 1024;  // what their registers let a compute unit hold
 
 template <typename RT, bool TAIL>
 hipError_t fwd(const NormFwdArgs &a, hipStream_t st) {
-  const int64_t v = (a.h + 7) / 8;
-  const unsigned grid = (unsigned)(a.M < (1 << 20) ? a.M : (1 << 20));
-  if (v <= 64) return launch(norm_fwd_kernel<RT, 64, 1, TAIL>, grid, 64, st, a);
-  if (v <= 256) return launch(norm_fwd_kernel<RT, 256, 1, TAIL>, grid, 256, st, a);
-  if (v <= 512) return launch(norm_fwd_kernel<RT, 512, 1, TAIL>, grid, 512, st, a);
-  if (v <= 1024) return launch(norm_fwd_kernel<RT, 1024, 1, TAIL>, grid, 1024, st, a);
-  return launch(norm_fwd_kernel<RT, 1024, 2, TAIL>, grid, 1024, st, a);
+  const unsigned grid = (unsigned)rows_grid(a.M, a.h, kFwdThreads), threads = (unsigned)row_threads(a.h);
+  return a.h <= 8192 ? launch(norm_fwd_kernel<RT, 1, TAIL>, grid, threads, st, a)
+                     : launch(norm_fwd_kernel<RT, 2, TAIL>, grid, threads, st, a);
 }
 
 template <typename RT, bool SUMS, bool TAIL>
 hipError_t bwd(const NormBwdArgs &a, float *part, hipStream_t st) {
-  const int64_t v = (a.h + 7) / 8;
-  const unsigned grid = SUMS ? (unsigned)bwd_grid(a.M, a.h) : (unsigned)(a.M < (1 << 20) ? a.M : (1 << 20));
-  if (v <= 64) return launch(norm_bwd_kernel<RT, 64, 1, SUMS, TAIL>, grid, 64, st, a, part);
-  if (v <= 256) return launch(norm_bwd_kernel<RT, 256, 1, SUMS, TAIL>, grid, 256, st, a, part);
-  if (v <= 512) return launch(norm_bwd_kernel<RT, 512, 1, SUMS, TAIL>, grid, 512, st, a, part);
-  if (v <= 1024) return launch(norm_bwd_kernel<RT, 1024, 1, SUMS, TAIL>, grid, 1024, st, a, part);
-  return launch(norm_bwd_kernel<RT, 1024, 2, SUMS, TAIL>, grid, 1024, st, a, part);
+  const unsigned grid = (unsigned)rows_grid(a.M, a.h, kBwdThreads), threads = (unsigned)row_threads(a.h);
+  return a.h <= 8192 ? launch(norm_bwd_kernel<RT, 1, SUMS, TAIL>, grid, threads, st, a, part)
+                     : launch(norm_bwd_kernel<RT, 2, SUMS, TAIL>, grid, threads, st, a, part);
 }
 
 template <typename RT>
@@ -423,7 +442,7 @@ hipError_t bwd_any(const NormBwdArgs &a, float *part, hipStream_t st) {
 
 }  // namespace
 
-size_t norm_bwd_workspace(int64_t M, int64_t h) { return (size_t)3 * bwd_grid(M, h) * h * 4; }
+size_t norm_bwd_workspace(int64_t M, int64_t h) { return (size_t)2 * rows_grid(M, h, kBwdThreads) * h * 4; }
 
 hipError_t launch_norm_fwd(const NormFwdArgs &a, bool r_bf16, hipStream_t st) {
   return r_bf16 ? fwd_any<uint16_t>(a, st) : fwd_any<float>(a, st);
@@ -434,9 +453,8 @@ hipError_t launch_norm_bwd(const NormBwdArgs &a, bool r_bf16, float *part, hipSt
     return r_bf16 ? bwd_any<uint16_t, false>(a, part, st) : bwd_any<float, false>(a, part, st);
   hipError_t e = r_bf16 ? bwd_any<uint16_t, true>(a, part, st) : bwd_any<float, true>(a, part, st);
   if (e != hipSuccess) return e;
-  const dim3 grid((unsigned)((a.h + 63) / 64), 3);
-  return launch(norm_sum_kernel, grid, 1024, st, (const float *)part, bwd_grid(a.M, a.h), a.h, a.dw_pre, a.dw_post,
-                a.dgate);
+  const dim3 grid((unsigned)((a.h + 63) / 64), 2);
+  return launch(norm_sum_kernel, grid, 1024, st, (const float *)part, rows_grid(a.M, a.h, kBwdThreads), a);
 }
 
 }  // namespace ql
