@@ -18,7 +18,7 @@
 // The arithmetic is float32; each output is rounded once.  N is formed from the
 // float32 r, not from the stored R_out: for a bf16 stream that saves N one rounding.
 // Rows need not be 16-byte aligned (any h): gfx950 takes 16-byte global accesses at
-// element alignment; a row's last h % 8 values go one by one.
+// element alignment, at a price, so an odd h's pieces begin on 16 bytes all the same.
 
 #include "norm.h"
 
@@ -34,29 +34,54 @@ typedef float f32x2_any __attribute__((ext_vector_type(2), aligned(4)));
 
 QL_DEV uint16_t nbf16(float v) { return (uint16_t)(pack_bf16x2(v, 0.0f) & 0xFFFFu); }
 
-// Eight values as they are in memory (bf16: 4 registers, float32: 8).  TAIL: h is not
-// a multiple of 8, and a row's last piece has n < 8 values, taken as 4, 2 and 1 of them
-// and zeros after them.
+// How a row divides into pieces of eight values.
+//   kWhole   h is a multiple of 8.
+//   kEdges   h > 8 is none: pieces begin on 16 bytes, but the first and the last lie wholly
+//            inside the row, so that every load is a wide one; they then overlap their
+//            neighbours, and count and store only their own values lo .. hi - 1.
+//   kTiny    h < 8: one piece, value by value.
+enum Rows { kWhole, kEdges, kTiny };
+
+template <Rows K>
+struct Cols {
+  int c, lo, hi;  // first column; own values; hi == 0: nothing of the row
+  // Piece `at` of rows whose first value is `skip` values into a 16-byte piece.
+  QL_DEV Cols(int at, int skip, int h) {
+    const int raw = 8 * at - skip;
+    if (K == kWhole) {
+      c = raw;
+      lo = 0;
+      hi = raw < h ? 8 : 0;
+    } else if (K == kEdges) {
+      c = raw < 0 ? 0 : raw > h - 8 ? h - 8 : raw;
+      lo = raw > h - 8 ? raw - c : 0;
+      hi = raw >= h ? 0 : raw < 0 ? 8 + raw : 8;
+    } else {
+      c = 0;
+      lo = 0;
+      hi = raw == 0 ? h : 0;
+    }
+  }
+  QL_DEV bool has(int i) const { return K == kWhole || (i >= lo && i < hi); }
+  QL_DEV bool whole() const { return K == kWhole || (K == kEdges && lo == 0 && hi == 8); }
+};
+
+// Eight values as they are in memory (bf16: 4 registers, float32: 8); zeros where !on.
 template <typename T>
 struct Piece;
 template <>
 struct Piece<uint16_t> {
   u32x4 v;
-  template <bool TAIL>
-  QL_DEV void load(const uint16_t *p, int n) {
+  template <Rows K>
+  QL_DEV void load(const uint16_t *row, const Cols<K> &q, bool on) {
     v = u32x4{0, 0, 0, 0};
-    if (TAIL ? n >= 8 : n > 0) {
-      v = *reinterpret_cast<const u32x4_any *>(p);
-    } else if (TAIL && n > 0) {
-      const bool four = n & 4, two = n & 2;
-      const uint32_t b = two ? *reinterpret_cast<const u32_any *>(p + (n & 4)) : 0u;
-      const uint32_t c = (n & 1) ? p[n & 6] : 0u;
-      if (four) {
-        const u32x2 a = *reinterpret_cast<const u32x2_any *>(p);
-        v = u32x4{a[0], a[1], two ? b : c, two ? c : 0u};
-      } else {
-        v = u32x4{two ? b : c, two ? c : 0u, 0u, 0u};
-      }
+    if (!on || q.hi == 0) return;
+    if (K != kTiny) {
+      v = *reinterpret_cast<const u32x4_any *>(row + q.c);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < q.hi) v[i >> 1] |= (uint32_t)row[i] << (16 * (i & 1));
     }
   }
   QL_DEV float get(int i) const { return (i & 1) ? bf16_hi(v[i >> 1]) : bf16_lo(v[i >> 1]); }
@@ -64,56 +89,45 @@ struct Piece<uint16_t> {
 template <>
 struct Piece<float> {
   f32x4 a, b;
-  template <bool TAIL>
-  QL_DEV void load(const float *p, int n) {
+  template <Rows K>
+  QL_DEV void load(const float *row, const Cols<K> &q, bool on) {
     a = f32x4{0, 0, 0, 0};
     b = f32x4{0, 0, 0, 0};
-    if (TAIL ? n >= 8 : n > 0) {
-      a = *reinterpret_cast<const f32x4_any *>(p);
-      b = *reinterpret_cast<const f32x4_any *>(p + 4);
-    } else if (TAIL && n > 0) {
-      f32x4 t = f32x4{0, 0, 0, 0};
-      const float one = (n & 1) ? p[n & 6] : 0.0f;
-      if (n & 2) {
-        const f32x2 w = *reinterpret_cast<const f32x2_any *>(p + (n & 4));
-        t = f32x4{w[0], w[1], one, 0};
-      } else {
-        t[0] = one;
-      }
-      if (n & 4) {
-        a = *reinterpret_cast<const f32x4_any *>(p);
-        b = t;
-      } else {
-        a = t;
-      }
+    if (!on || q.hi == 0) return;
+    if (K != kTiny) {
+      a = *reinterpret_cast<const f32x4_any *>(row + q.c);
+      b = *reinterpret_cast<const f32x4_any *>(row + q.c + 4);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < q.hi) (i < 4 ? a : b)[i & 3] = row[i];
     }
   }
   QL_DEV float get(int i) const { return i < 4 ? a[i & 3] : b[i & 3]; }
 };
 
-template <bool TAIL>
-QL_DEV void store8(uint16_t *p, const float (&x)[8], int n) {
+template <Rows K>
+QL_DEV void store8(uint16_t *row, const float (&x)[8], const Cols<K> &q) {
+  if (q.hi == 0) return;
   const u32x4 v{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
-  if (!TAIL || n >= 8) {
-    *reinterpret_cast<u32x4_any *>(p) = v;
+  if (q.whole()) {
+    *reinterpret_cast<u32x4_any *>(row + q.c) = v;
   } else {
-    if (n & 4) *reinterpret_cast<u32x2_any *>(p) = u32x2{v[0], v[1]};
-    const uint32_t b = (n & 4) ? v[2] : v[0], c = (n & 2) ? ((n & 4) ? v[3] : v[1]) : b;
-    if (n & 2) *reinterpret_cast<u32_any *>(p + (n & 4)) = b;
-    if (n & 1) p[n & 6] = (uint16_t)c;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (q.has(i)) row[q.c + i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
   }
 }
-template <bool TAIL>
-QL_DEV void store8(float *p, const float (&x)[8], int n) {
-  const f32x4 a{x[0], x[1], x[2], x[3]}, b{x[4], x[5], x[6], x[7]};
-  if (!TAIL || n >= 8) {
-    *reinterpret_cast<f32x4_any *>(p) = a;
-    *reinterpret_cast<f32x4_any *>(p + 4) = b;
+template <Rows K>
+QL_DEV void store8(float *row, const float (&x)[8], const Cols<K> &q) {
+  if (q.hi == 0) return;
+  if (q.whole()) {
+    *reinterpret_cast<f32x4_any *>(row + q.c) = f32x4{x[0], x[1], x[2], x[3]};
+    *reinterpret_cast<f32x4_any *>(row + q.c + 4) = f32x4{x[4], x[5], x[6], x[7]};
   } else {
-    if (n & 4) *reinterpret_cast<f32x4_any *>(p) = a;
-    const f32x4 t = (n & 4) ? b : a;
-    if (n & 2) *reinterpret_cast<f32x2_any *>(p + (n & 4)) = f32x2{t[0], t[1]};
-    if (n & 1) p[n & 6] = (n & 2) ? t[2] : t[0];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (q.has(i)) row[q.c + i] = x[i];
   }
 }
 
@@ -151,11 +165,11 @@ QL_DEV float wg_sum(float v, float *red, int nw) {
 }  // namespace
 
 // Eight weights; ones where there are none (a product with 1 changes nothing).
-template <bool TAIL>
-QL_DEV Piece<float> weights(const float *w, int c, int h) {
+template <Rows K>
+QL_DEV Piece<float> weights(const float *w, const Cols<K> &q) {
   Piece<float> p;
   if (w) {
-    p.load<TAIL>(w + (c < h ? c : 0), c < h ? h - c : 0);
+    p.load(w, q, true);
   } else {
     p.a = f32x4{1, 1, 1, 1};
     p.b = f32x4{1, 1, 1, 1};
@@ -163,15 +177,22 @@ QL_DEV Piece<float> weights(const float *w, int c, int h) {
   return p;
 }
 
+// Where in a 16-byte piece a workgroup's rows begin (`shift` is 7, or 0 for pieces that
+// begin with the row): all its rows are a multiple of 8 apart, so it is one place.
+template <Rows K>
+QL_DEV int row_skip(int h, int shift) {
+  return K == kEdges ? (int)(((int64_t)blockIdx.x * h) & shift) : 0;
+}
+
 // NV pieces of eight values per thread, whole waves (8 NV blockDim >= h).  A workgroup walks
 // the rows blockIdx.x, + gridDim.x, ...: its weights stay in registers (alpha * gate *
 // w_post as one), and the next row is loaded before this one's sums, whose barriers would
 // otherwise leave the memory idle.
-template <typename RT, int NV, bool TAIL>
-__global__ __launch_bounds__(1024) void norm_fwd_kernel(NormFwdArgs p) {
+template <typename RT, int NV, Rows K>
+__global__ __launch_bounds__(1024) void norm_fwd_kernel(NormFwdArgs p, int shift) {
   __shared__ float red[4][kMaxWaves];
   const int tid = threadIdx.x, B = blockDim.x, nw = B >> 6;
-  const int h = (int)p.h;
+  const int h = (int)p.h, skip = row_skip<K>(h, shift);
   const RT *R = reinterpret_cast<const RT *>(p.R);
   RT *Ro = reinterpret_cast<RT *>(p.R_out);
   const float inv_h = 1.0f / (float)h;
@@ -179,9 +200,9 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormFwdArgs p) {
   float a[NV][8];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int c = 8 * (tid + B * j);
-    const Piece<float> wq = weights<TAIL>(p.w_post, c, h), wg = weights<TAIL>(p.gate, c, h);
-    wp[j] = weights<TAIL>(p.w_pre, c, h);
+    const Cols<K> q(tid + B * j, skip, h);
+    const Piece<float> wq = weights(p.w_post, q), wg = weights(p.gate, q);
+    wp[j] = weights(p.w_pre, q);
 #pragma unroll
     for (int i = 0; i < 8; ++i) a[j][i] = p.alpha * wg.get(i) * wq.get(i);
   }
@@ -190,10 +211,9 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormFwdArgs p) {
   auto load = [&](int64_t m) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = 8 * (tid + B * j), n = m < p.M && c < h ? h - c : 0;
-      const int64_t at = n ? m * h + c : 0;
-      rr[j].template load<TAIL>(R + at, n);
-      yy[j].template load<TAIL>(p.Y + at, p.Y ? n : 0);
+      const Cols<K> q(tid + B * j, skip, h);
+      rr[j].load(R + m * h, q, m < p.M);
+      yy[j].load(p.Y + m * h, q, m < p.M && p.Y);
     }
   };
   load(blockIdx.x);
@@ -201,12 +221,14 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormFwdArgs p) {
   for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
     float r[NV][8], u[NV][8];
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
+      const Cols<K> q(tid + B * j, skip, h);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        r[j][i] = rr[j].get(i);
-        u[j][i] = yy[j].get(i);
+        r[j][i] = q.has(i) ? rr[j].get(i) : 0.0f;
+        u[j][i] = q.has(i) ? yy[j].get(i) : 0.0f;
       }
+    }
     load(m + gridDim.x);
     if (p.Y) {
       float rs = 1.0f;
@@ -222,10 +244,10 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormFwdArgs p) {
       }
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int c = 8 * (tid + B * j);
+        const Cols<K> q(tid + B * j, skip, h);
 #pragma unroll
         for (int i = 0; i < 8; ++i) r[j][i] = __builtin_fmaf(a[j][i], u[j][i] * rs, r[j][i]);
-        if (c < h) store8<TAIL>(Ro + m * h + c, r[j], h - c);
+        store8(Ro + m * h, r[j], q);
       }
     }
     if (p.w_pre) {
@@ -239,11 +261,11 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormFwdArgs p) {
       if (p.rstd_pre && tid == 0) p.rstd_pre[m] = rs;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int c = 8 * (tid + B * j);
+        const Cols<K> q(tid + B * j, skip, h);
         float o[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] = r[j][i] * rs * wp[j].get(i);
-        if (c < h) store8<TAIL>(p.N + m * h + c, o, h - c);
+        store8(p.N + m * h, o, q);
       }
     }
   }
@@ -255,12 +277,12 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormFwdArgs p) {
 // of part[2][gridDim.x][h] (norm_sum_kernel adds the rows in a fixed order: no atomics, the
 // same bits every time).  The next row is loaded before this one's sums where one piece per
 // thread holds a row (h <= 8192); wider rows have no registers left for it.
-template <typename RT, int NV, bool SUMS, bool TAIL>
-__global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs p, float *__restrict__ part) {
+template <typename RT, int NV, bool SUMS, Rows K>
+__global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs p, int shift, float *__restrict__ part) {
   constexpr bool AHEAD = NV == 1;
   __shared__ float red[4][kMaxWaves];
   const int tid = threadIdx.x, B = blockDim.x, nw = B >> 6;
-  const int h = (int)p.h;
+  const int h = (int)p.h, skip = row_skip<K>(h, shift);
   const RT *Ro = reinterpret_cast<const RT *>(p.R_out), *dRo = reinterpret_cast<const RT *>(p.dR_out);
   RT *dR = reinterpret_cast<RT *>(p.dR);
   const float inv_h = 1.0f / (float)h;
@@ -274,9 +296,9 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs p, float *__
   float a[NV][8];  // alpha * gate * w_post
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int c = 8 * (tid + B * j);
-    const Piece<float> wq = weights<TAIL>(p.w_post, c, h), wg = weights<TAIL>(p.gate, c, h);
-    wp[j] = weights<TAIL>(p.w_pre, c, h);
+    const Cols<K> q(tid + B * j, skip, h);
+    const Piece<float> wq = weights(p.w_post, q), wg = weights(p.gate, q);
+    wp[j] = weights(p.w_pre, q);
 #pragma unroll
     for (int i = 0; i < 8; ++i) a[j][i] = p.alpha * wg.get(i) * wq.get(i);
   }
@@ -287,12 +309,11 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs p, float *__
     const bool in = m < p.M;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = 8 * (tid + B * j), n = in && c < h ? h - c : 0;
-      const int64_t at = n ? m * h + c : 0;
-      dn[j].template load<TAIL>(p.dN + at, p.dN ? n : 0);
-      ro[j].template load<TAIL>(Ro + at, p.w_pre ? n : 0);
-      dro[j].template load<TAIL>(dRo + at, dRo ? n : 0);
-      yy[j].template load<TAIL>(p.Y + at, p.Y ? n : 0);
+      const Cols<K> q(tid + B * j, skip, h);
+      dn[j].load(p.dN + m * h, q, in && p.dN);
+      ro[j].load(Ro + m * h, q, in && p.w_pre);
+      dro[j].load(dRo + m * h, q, in && dRo);
+      yy[j].load(p.Y + m * h, q, in && p.Y);
     }
     rsp = in && p.w_pre ? p.rstd_pre[m] : 0.0f;
     rsq = in && p.w_post ? p.rstd_post[m] : 1.0f;
@@ -304,17 +325,19 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs p, float *__
     const float rp = rsp, rq = rsq;
     float dot = 0.0f;
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
+      const Cols<K> q(tid + B * j, skip, h);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float g = dn[j].get(i);
-        x[j][i] = ro[j].get(i) * rp;
-        y[j][i] = yy[j].get(i) * rq;
+        const float g = q.has(i) ? dn[j].get(i) : 0.0f;
+        x[j][i] = q.has(i) ? ro[j].get(i) * rp : 0.0f;
+        y[j][i] = q.has(i) ? yy[j].get(i) * rq : 0.0f;
         d[j][i] = g * wp[j].get(i);
-        dr[j][i] = dro[j].get(i);
+        dr[j][i] = q.has(i) ? dro[j].get(i) : 0.0f;
         dot = __builtin_fmaf(d[j][i], x[j][i], dot);
         if (SUMS) s_pre[SUMS ? j : 0][i] = __builtin_fmaf(g, x[j][i], s_pre[SUMS ? j : 0][i]);
       }
+    }
     if (AHEAD) load(m + gridDim.x);
     if (p.w_pre) {
       dot = wg_sum(dot, red[slot], nw) * inv_h;
@@ -326,8 +349,8 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs p, float *__
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = 8 * (tid + B * j);
-      if (c < h) store8<TAIL>(dR + m * h + c, dr[j], h - c);
+      const Cols<K> q(tid + B * j, skip, h);
+      store8(dR + m * h, dr[j], q);
     }
     if (p.dY) {
       dot = 0.0f;
@@ -350,8 +373,8 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs p, float *__
       }
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int c = 8 * (tid + B * j);
-        if (c < h) store8<TAIL>(p.dY + m * h + c, dr[j], h - c);
+        const Cols<K> q(tid + B * j, skip, h);
+        store8(p.dY + m * h, dr[j], q);
       }
     }
     if (!AHEAD) load(m + gridDim.x);
@@ -361,10 +384,9 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs p, float *__
     float *out = part + (int64_t)blockIdx.x * h;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = 8 * (tid + B * j);
-      if (c >= h) continue;
-      if (p.dw_pre) store8<TAIL>(out + c, s_pre[j], h - c);
-      if (p.dw_post || p.dgate) store8<TAIL>(out + plane + c, s_y[j], h - c);
+      const Cols<K> q(tid + B * j, skip, h);
+      if (p.dw_pre) store8(out, s_pre[j], q);
+      if (p.dw_post || p.dgate) store8(out + plane, s_y[j], q);
     }
   }
 }
@@ -405,39 +427,48 @@ __global__ __launch_bounds__(1024) void norm_sum_kernel(const float *__restrict_
 
 namespace {
 
-// Threads per row: one piece each up to 8192 values, two beyond, in whole waves.
+// Pieces that a row takes: with h no multiple of 8, up to 7 values before the row's first
+// (its pieces then begin on 16 bytes) unless the row fills the workgroup without them.
+constexpr int64_t kMaxPieces = kMaxNormWidth / 8;
+int row_shift(int64_t h) { return h % 8 && h > 8 && (h + 14) / 8 <= kMaxPieces ? 7 : 0; }
+int64_t row_pieces(int64_t h) { return (h + row_shift(h) + 7) / 8; }
+// Threads per row: one piece each up to 1024 pieces, two beyond, in whole waves.
 int row_threads(int64_t h) {
-  const int64_t v = (h + 7) / 8, t = v <= 1024 ? v : (v + 1) / 2;
+  const int64_t v = row_pieces(h), t = v <= 1024 ? v : (v + 1) / 2;
   return (int)((t + 63) / 64 * 64);
 }
-// Workgroups for M rows: `threads` per compute unit.
+// Workgroups for M rows: one a row, or `threads` per compute unit (a multiple of 8 workgroups).
 int rows_grid(int64_t M, int64_t h, int threads) {
   const int64_t per = 256 * (int64_t)(threads / row_threads(h));
   return (int)(M < per ? M : per);
 }
 constexpr int kFwdThreads = 2048, kBwdThreads = 1024;  // what their registers let a compute unit hold
 
-template <typename RT, bool TAIL>
+template <typename RT, Rows K>
 hipError_t fwd(const NormFwdArgs &a, hipStream_t st) {
   const unsigned grid = (unsigned)rows_grid(a.M, a.h, kFwdThreads), threads = (unsigned)row_threads(a.h);
-  return a.h <= 8192 ? launch(norm_fwd_kernel<RT, 1, TAIL>, grid, threads, st, a)
-                     : launch(norm_fwd_kernel<RT, 2, TAIL>, grid, threads, st, a);
+  const int shift = row_shift(a.h);
+  return row_pieces(a.h) <= 1024 ? launch(norm_fwd_kernel<RT, 1, K>, grid, threads, st, a, shift)
+                                 : launch(norm_fwd_kernel<RT, K == kTiny ? 1 : 2, K>, grid, threads, st, a, shift);
 }
 
-template <typename RT, bool SUMS, bool TAIL>
+template <typename RT, bool SUMS, Rows K>
 hipError_t bwd(const NormBwdArgs &a, float *part, hipStream_t st) {
   const unsigned grid = (unsigned)rows_grid(a.M, a.h, kBwdThreads), threads = (unsigned)row_threads(a.h);
-  return a.h <= 8192 ? launch(norm_bwd_kernel<RT, 1, SUMS, TAIL>, grid, threads, st, a, part)
-                     : launch(norm_bwd_kernel<RT, 2, SUMS, TAIL>, grid, threads, st, a, part);
+  const int shift = row_shift(a.h);
+  return row_pieces(a.h) <= 1024 ? launch(norm_bwd_kernel<RT, 1, SUMS, K>, grid, threads, st, a, shift, part)
+                                 : launch(norm_bwd_kernel<RT, K == kTiny ? 1 : 2, SUMS, K>, grid, threads, st, a, shift, part);
 }
 
 template <typename RT>
 hipError_t fwd_any(const NormFwdArgs &a, hipStream_t st) {
-  return a.h % 8 ? fwd<RT, true>(a, st) : fwd<RT, false>(a, st);
+  return a.h % 8 == 0 ? fwd<RT, kWhole>(a, st) : a.h > 8 ? fwd<RT, kEdges>(a, st) : fwd<RT, kTiny>(a, st);
 }
 template <typename RT, bool SUMS>
 hipError_t bwd_any(const NormBwdArgs &a, float *part, hipStream_t st) {
-  return a.h % 8 ? bwd<RT, SUMS, true>(a, part, st) : bwd<RT, SUMS, false>(a, part, st);
+  return a.h % 8 == 0 ? bwd<RT, SUMS, kWhole>(a, part, st)
+         : a.h > 8    ? bwd<RT, SUMS, kEdges>(a, part, st)
+                      : bwd<RT, SUMS, kTiny>(a, part, st);
 }
 
 }  // namespace
