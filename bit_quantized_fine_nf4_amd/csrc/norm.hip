@@ -189,7 +189,7 @@ QL_DEV int row_skip(int h, int shift) {
 // w_post as one), and the next row is loaded before this one's sums, whose barriers would
 // otherwise leave the memory idle.
 template <typename RT, int NV, Rows K>
-__global__ __launch_bounds__(1024) void norm_fwd_kernel(NormFwdArgs p, int shift) {
+__global__ __launch_bounds__(512) void norm_fwd_kernel(NormFwdArgs p, int shift) {
   __shared__ float red[4][kMaxWaves];
   const int tid = threadIdx.x, B = blockDim.x, nw = B >> 6;
   const int h = (int)p.h, skip = row_skip<K>(h, shift);
@@ -286,12 +286,19 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs p, int shift
   const RT *Ro = reinterpret_cast<const RT *>(p.R_out), *dRo = reinterpret_cast<const RT *>(p.dR_out);
   RT *dR = reinterpret_cast<RT *>(p.dR);
   const float inv_h = 1.0f / (float)h;
-  constexpr int NS = SUMS ? NV : 1;
-  float s_pre[NS][8], s_y[NS][8];
+  // this thread's column sums: registers, or with two pieces LDS (they would spill)
+  constexpr bool IN_LDS = SUMS && NV == 2;
+  __shared__ float sums[IN_LDS ? 2 * NV * 8 * 1024 : 1];
+  float s_pre[SUMS && !IN_LDS ? NV : 1][8], s_y[SUMS && !IN_LDS ? NV : 1][8];
+  auto sum = [&](int which, int j, int i) -> float & {
+    if constexpr (IN_LDS) return sums[((which * NV + j) * 8 + i) * 1024 + tid];
+    return which ? s_y[j][i] : s_pre[j][i];
+  };
+  if constexpr (SUMS)
 #pragma unroll
-  for (int j = 0; j < NS; ++j)
+    for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s_pre[j][i] = s_y[j][i] = 0.0f;
+      for (int i = 0; i < 8; ++i) sum(0, j, i) = sum(1, j, i) = 0.0f;
   Piece<float> wp[NV];
   float a[NV][8];  // alpha * gate * w_post
 #pragma unroll
@@ -335,7 +342,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs p, int shift
         d[j][i] = g * wp[j].get(i);
         dr[j][i] = q.has(i) ? dro[j].get(i) : 0.0f;
         dot = __builtin_fmaf(d[j][i], x[j][i], dot);
-        if (SUMS) s_pre[SUMS ? j : 0][i] = __builtin_fmaf(g, x[j][i], s_pre[SUMS ? j : 0][i]);
+        if constexpr (SUMS) sum(0, j, i) = __builtin_fmaf(g, x[j][i], sum(0, j, i));
       }
     }
     if (AHEAD) load(m + gridDim.x);
@@ -359,7 +366,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs p, int shift
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           // without a norm after the block y is Y, and the gradient ends here
-          if (SUMS) s_y[SUMS ? j : 0][i] = __builtin_fmaf(dr[j][i], y[j][i], s_y[SUMS ? j : 0][i]);
+          if constexpr (SUMS) sum(1, j, i) = __builtin_fmaf(dr[j][i], y[j][i], sum(1, j, i));
           dr[j][i] *= a[j][i];
           dot = __builtin_fmaf(dr[j][i], y[j][i], dot);
         }
@@ -385,8 +392,14 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs p, int shift
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const Cols<K> q(tid + B * j, skip, h);
-      if (p.dw_pre) store8(out, s_pre[j], q);
-      if (p.dw_post || p.dgate) store8(out + plane, s_y[j], q);
+      float v[2][8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[0][i] = sum(0, j, i);
+        v[1][i] = sum(1, j, i);
+      }
+      if (p.dw_pre) store8(out, v[0], q);
+      if (p.dw_post || p.dgate) store8(out + plane, v[1], q);
     }
   }
 }
@@ -432,32 +445,43 @@ namespace {
 constexpr int64_t kMaxPieces = kMaxNormWidth / 8;
 int row_shift(int64_t h) { return h % 8 && h > 8 && (h + 14) / 8 <= kMaxPieces ? 7 : 0; }
 int64_t row_pieces(int64_t h) { return (h + row_shift(h) + 7) / 8; }
-// Threads per row: one piece each up to 1024 pieces, two beyond, in whole waves.
-int row_threads(int64_t h) {
-  const int64_t v = row_pieces(h), t = v <= 1024 ? v : (v + 1) / 2;
-  return (int)((t + 63) / 64 * 64);
+// Pieces per thread and threads per row, in whole waves.  Forward, at most 512 threads: two
+// rows' workgroups to a compute unit, eight waves at a barrier (2048 x 8192: 21.9 us, with
+// 1024 threads of one piece 29 to 32).  Backward, at most 1024: two pieces' operands, sums
+// and prefetches take 200 registers, and the compute unit then holds half the threads
+// (1777 x 5003: 39 us for 27).
+struct RowShape {
+  int depth, threads, grid;
+};
+RowShape row_shape(int64_t M, int64_t h, int most) {
+  const int64_t v = row_pieces(h);
+  RowShape s;
+  s.depth = v <= most ? 1 : v <= 2 * most ? 2 : 4;
+  s.threads = (int)((v + 64 * s.depth - 1) / (64 * s.depth) * 64);
+  const int64_t fill = 256 * (int64_t)((s.depth == 4 ? 512 : 1024) / s.threads);  // workgroups, a multiple of 8
+  s.grid = (int)(M < fill ? M : fill);
+  return s;
 }
-// Workgroups for M rows: one a row, or `threads` per compute unit (a multiple of 8 workgroups).
-int rows_grid(int64_t M, int64_t h, int threads) {
-  const int64_t per = 256 * (int64_t)(threads / row_threads(h));
-  return (int)(M < per ? M : per);
-}
-constexpr int kFwdThreads = 2048, kBwdThreads = 1024;  // what their registers let a compute unit hold
+constexpr int kFwdThreads = 512, kBwdThreads = 1024;
 
 template <typename RT, Rows K>
 hipError_t fwd(const NormFwdArgs &a, hipStream_t st) {
-  const unsigned grid = (unsigned)rows_grid(a.M, a.h, kFwdThreads), threads = (unsigned)row_threads(a.h);
+  const RowShape s = row_shape(a.M, a.h, kFwdThreads);
   const int shift = row_shift(a.h);
-  return row_pieces(a.h) <= 1024 ? launch(norm_fwd_kernel<RT, 1, K>, grid, threads, st, a, shift)
-                                 : launch(norm_fwd_kernel<RT, K == kTiny ? 1 : 2, K>, grid, threads, st, a, shift);
+  if constexpr (K != kTiny) {
+    if (s.depth == 4) return launch(norm_fwd_kernel<RT, 4, K>, s.grid, s.threads, st, a, shift);
+    if (s.depth == 2) return launch(norm_fwd_kernel<RT, 2, K>, s.grid, s.threads, st, a, shift);
+  }
+  return launch(norm_fwd_kernel<RT, 1, K>, s.grid, s.threads, st, a, shift);
 }
 
 template <typename RT, bool SUMS, Rows K>
 hipError_t bwd(const NormBwdArgs &a, float *part, hipStream_t st) {
-  const unsigned grid = (unsigned)rows_grid(a.M, a.h, kBwdThreads), threads = (unsigned)row_threads(a.h);
+  const RowShape s = row_shape(a.M, a.h, kBwdThreads);
   const int shift = row_shift(a.h);
-  return row_pieces(a.h) <= 1024 ? launch(norm_bwd_kernel<RT, 1, SUMS, K>, grid, threads, st, a, shift, part)
-                                 : launch(norm_bwd_kernel<RT, K == kTiny ? 1 : 2, SUMS, K>, grid, threads, st, a, shift, part);
+  if constexpr (K != kTiny)
+    if (s.depth == 2) return launch(norm_bwd_kernel<RT, 2, SUMS, K>, s.grid, s.threads, st, a, shift, part);
+  return launch(norm_bwd_kernel<RT, 1, SUMS, K>, s.grid, s.threads, st, a, shift, part);
 }
 
 template <typename RT>
@@ -473,7 +497,7 @@ hipError_t bwd_any(const NormBwdArgs &a, float *part, hipStream_t st) {
 
 }  // namespace
 
-size_t norm_bwd_workspace(int64_t M, int64_t h) { return (size_t)2 * rows_grid(M, h, kBwdThreads) * h * 4; }
+size_t norm_bwd_workspace(int64_t M, int64_t h) { return (size_t)2 * row_shape(M, h, kBwdThreads).grid * h * 4; }
 
 hipError_t launch_norm_fwd(const NormFwdArgs &a, bool r_bf16, hipStream_t st) {
   return r_bf16 ? fwd_any<uint16_t>(a, st) : fwd_any<float>(a, st);
@@ -485,7 +509,7 @@ hipError_t launch_norm_bwd(const NormBwdArgs &a, bool r_bf16, float *part, hipSt
   hipError_t e = r_bf16 ? bwd_any<uint16_t, true>(a, part, st) : bwd_any<float, true>(a, part, st);
   if (e != hipSuccess) return e;
   const dim3 grid((unsigned)((a.h + 63) / 64), 2);
-  return launch(norm_sum_kernel, grid, 1024, st, (const float *)part, rows_grid(a.M, a.h, kBwdThreads), a);
+  return launch(norm_sum_kernel, grid, 1024, st, (const float *)part, row_shape(a.M, a.h, kBwdThreads).grid, a);
 }
 
 }  // namespace ql
