@@ -118,24 +118,29 @@ def _dev_check(*ts):
             raise ValueError("tensors must be contiguous and on the GPU")
 
 
-def _want(name: str, t: Optional[torch.Tensor], dtype, shape, device):
+def _want(name: str, t: Optional[torch.Tensor], dtype, shape: tuple, device):
     """Refuses a tensor that the C call would misread: its type, shape, layout or device."""
     if t is None:
         return
-    if not t.is_cuda or t.device != device or not t.is_contiguous():
+    if t.get_device() != device.index or not t.is_contiguous():  # (a CPU tensor: -1 and None)
         raise ValueError(f"{name} must be contiguous and on {device}")
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name} is {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+
+
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def _call(device, name: str, *args):
     """Entry point `name` on `device`'s current stream, with that device current."""
-    stream = _stream(device)
-    if torch.cuda.current_device() == device.index:
-        _check(getattr(lib, name)(*args, stream), name)
+    stream = torch._C._cuda_getCurrentRawStream(device.index)
+    if torch._C._cuda_getDevice() == device.index:
+        status = getattr(lib, name)(*args, stream)
     else:
         with torch.cuda.device(device):
-            _check(getattr(lib, name)(*args, stream), name)
+            status = getattr(lib, name)(*args, stream)
+    _check(status, name)
 
 
 def nf4_levels() -> list:
@@ -475,8 +480,8 @@ def qlora_norm_fwd(R: torch.Tensor, Y: Optional[torch.Tensor] = None, w_pre: Opt
                                   ("gate", gate, torch.float32, (h,)), ("rstd_pre", rstd_pre, torch.float32, (M,)),
                                   ("rstd_post", rstd_post, torch.float32, (M,))):
         _want(name, t, dtype, shape, dev)
-    _call(dev, "qlora_norm_fwd", _ptr(R), dt, _ptr(Y), _ptr(w_post), _ptr(gate), float(alpha), _ptr(w_pre),
-          float(eps), M, h, _ptr(R_out), _ptr(N), _ptr(rstd_post), _ptr(rstd_pre))
+    _call(dev, "qlora_norm_fwd", _at(R), dt, _at(Y), _at(w_post), _at(gate), float(alpha), _at(w_pre),
+          float(eps), M, h, _at(R_out), _at(N), _at(rstd_post), _at(rstd_pre))
     return R_out, N, rstd_pre, rstd_post
 
 
@@ -518,9 +523,9 @@ def qlora_norm_bwd(dN: Optional[torch.Tensor], dR_out: Optional[torch.Tensor], R
                                   ("workspace", workspace, torch.uint8,
                                    () if workspace is None else (workspace.numel(),))):
         _want(name, t, dtype, shape, dev)
-    _call(dev, "qlora_norm_bwd", _ptr(dN), _ptr(dR_out), dt, _ptr(R_out), _ptr(Y if block else None),
-          _ptr(rstd_post), _ptr(rstd_pre), _ptr(w_post), _ptr(gate), float(alpha), _ptr(w_pre), M, h, _ptr(dR),
-          _ptr(dY), _ptr(dw_pre), _ptr(dw_post), _ptr(dgate), _ptr(workspace),
+    _call(dev, "qlora_norm_bwd", _at(dN), _at(dR_out), dt, _at(R_out), _at(Y if block else None),
+          _at(rstd_post), _at(rstd_pre), _at(w_post), _at(gate), float(alpha), _at(w_pre), M, h, _at(dR),
+          _at(dY), _at(dw_pre), _at(dw_post), _at(dgate), _at(workspace),
           0 if workspace is None else workspace.numel())
     return dR, dY, dw_pre, dw_post, dgate
 
@@ -555,7 +560,7 @@ def qlora_loss_fwd(H: torch.Tensor, W: torch.Tensor, labels: torch.Tensor, loss:
                                   ("lse", lse, torch.float32, (M,))):
         _want(name, t, dtype, shape, dev)
     ws = _workspace(QLORA_OP_LOSS_FWD, workspace, dev, M, h, V)
-    _call(dev, "qlora_loss_fwd", _ptr(H), _ptr(W), _ptr(labels), M, h, V, _ptr(loss), _ptr(lse), _ptr(ws), ws.numel())
+    _call(dev, "qlora_loss_fwd", _at(H), _at(W), _at(labels), M, h, V, _at(loss), _at(lse), _at(ws), ws.numel())
     return loss, lse
 
 
@@ -575,8 +580,8 @@ def qlora_loss_bwd(H: torch.Tensor, W: torch.Tensor, labels: torch.Tensor, lse: 
                                   ("dW", dW, torch.bfloat16, (V, h))):
         _want(name, t, dtype, shape, dev)
     ws = _workspace(QLORA_OP_LOSS_BWD, workspace, dev, M, h, V)
-    _call(dev, "qlora_loss_bwd", _ptr(H), _ptr(W), _ptr(labels), _ptr(lse), _ptr(dloss), M, h, V, _ptr(dH), _ptr(dW),
-          _ptr(ws), ws.numel())
+    _call(dev, "qlora_loss_bwd", _at(H), _at(W), _at(labels), _at(lse), _at(dloss), M, h, V, _at(dH), _at(dW),
+          _at(ws), ws.numel())
     return dH, dW
 
 
@@ -586,7 +591,7 @@ def qlora_loss_bwd(H: torch.Tensor, W: torch.Tensor, labels: torch.Tensor, lse: 
 
 def _rng_state(rng: torch.Tensor, device):
     _want("rng", rng, torch.int64, (2,), device)
-    return _ptr(rng)
+    return rng.data_ptr()
 
 
 def qlora_dropout(x: torch.Tensor, p: float, rng: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -598,8 +603,8 @@ def qlora_dropout(x: torch.Tensor, p: float, rng: torch.Tensor, out: Optional[to
     out = torch.empty_like(x) if out is None else out
     _want("x", x, x.dtype, x.shape, x.device)
     _want("out", out, x.dtype, x.shape, x.device)
-    _call(x.device, "qlora_dropout", _ptr(x), _STREAM_TYPES[x.dtype], x.numel(), float(p), _rng_state(rng, x.device),
-          _ptr(out))
+    _call(x.device, "qlora_dropout", _at(x), _STREAM_TYPES[x.dtype], x.numel(), float(p), _rng_state(rng, x.device),
+          _at(out))
     return out
 
 
@@ -621,7 +626,7 @@ def _drop_workspace(given, dev, M, W, r):
     if given is None and workspace_size(QLORA_OP_LINEAR_DROPOUT, M, W.h, W.o, r) == 0:
         return None, 0
     ws = _workspace(QLORA_OP_LINEAR_DROPOUT, given, dev, M, W.h, W.o, r)
-    return _ptr(ws), ws.numel()
+    return _at(ws), ws.numel()
 
 
 def qlora_linear_fwd_dropout(W: NF4Weight, X: torch.Tensor, L1: Optional[torch.Tensor], L2: Optional[torch.Tensor],
@@ -633,8 +638,8 @@ def qlora_linear_fwd_dropout(W: NF4Weight, X: torch.Tensor, L1: Optional[torch.T
     Y = torch.empty(M, W.o, dtype=torch.bfloat16, device=dev) if Y is None else Y
     T = torch.empty(M, r, dtype=torch.bfloat16, device=dev) if T is None and r else T
     ws, wb = _drop_workspace(workspace, dev, M, W, r)
-    _call(dev, "qlora_linear_fwd_dropout", ctypes.byref(W.as_ctypes()), W.codebook, _ptr(X), M, _ptr(L1), _ptr(L2), r,
-          float(s), float(p), _rng_state(rng, dev), _ptr(Y), _ptr(T), ws, wb)
+    _call(dev, "qlora_linear_fwd_dropout", ctypes.byref(W.as_ctypes()), W.codebook, _at(X), M, _at(L1), _at(L2), r,
+          float(s), float(p), _rng_state(rng, dev), _at(Y), _at(T), ws, wb)
     return Y, T
 
 
@@ -653,6 +658,6 @@ def qlora_linear_bwd_dropout(W: NF4Weight, X: torch.Tensor, T: Optional[torch.Te
         dL1 = torch.empty(W.h, r, dtype=torch.float32, device=dev) if dL1 is None else dL1
         dL2 = torch.empty(r, W.o, dtype=torch.float32, device=dev) if dL2 is None else dL2
     ws, wb = _drop_workspace(workspace, dev, M, W, r)
-    _call(dev, "qlora_linear_bwd_dropout", ctypes.byref(W.as_ctypes()), W.codebook, _ptr(X), _ptr(T), _ptr(dY), M,
-          _ptr(L1), _ptr(L2), r, float(s), float(p), _rng_state(rng, dev), _ptr(dX), _ptr(dL1), _ptr(dL2), ws, wb)
+    _call(dev, "qlora_linear_bwd_dropout", ctypes.byref(W.as_ctypes()), W.codebook, _at(X), _at(T), _at(dY), M,
+          _at(L1), _at(L2), r, float(s), float(p), _rng_state(rng, dev), _at(dX), _at(dL1), _at(dL2), ws, wb)
     return dX, dL1, dL2

@@ -19,7 +19,8 @@
 // on the GPU only: launches are sized for all M tokens and the surplus workgroups leave.
 //
 // Kernels: loss_select_kernel (one workgroup: the compact list), loss_gather_kernel
-// (the copy; zeroes the skipped rows of dH), the products of loss_gemm.hip,
+// (the copy; zeroes the skipped rows of dH), both as loss_collect_kernel where the tokens
+// are few, the products of loss_gemm.hip,
 // loss_finish_kernel (lse and loss from the tiles' statistics), loss_dh_kernel (sums
 // dH's partials and rounds).  Everything is added in a fixed order: no atomics.
 
@@ -124,6 +125,96 @@ __global__ __launch_bounds__(256) void loss_gather_kernel(const uint16_t *H, int
       u32x4 *dst = reinterpret_cast<u32x4 *>(dH + i * h);
       for (int64_t c = lane; c < h / 8; c += 64) dst[c] = u32x4{0, 0, 0, 0};
     }
+  }
+}
+
+// loss_select_kernel and loss_gather_kernel in one, for at most kCollect tokens: every
+// workgroup makes the list for itself (the labels are a few KB) and copies its share of
+// the rows; workgroup 0 also stores the list.  At 16 tokens of 4096 values the two took
+// 9 us and a wait between launches, this one 4.8 us.
+constexpr int kCollect = 1024;
+__global__ __launch_bounds__(256) void loss_collect_kernel(const uint16_t *H, const int64_t *labels, int64_t M,
+                                                           int64_t h, int64_t V, int *count, int *idx, int *label,
+                                                           const float *lse, const float *dloss, float *c_lse,
+                                                           float *c_dloss, float *c_top, float *out_loss,
+                                                           float *out_lse, uint16_t *Hc, uint16_t *dH) {
+  constexpr int kWaves = 4, kPer = kCollect / 256;
+  __shared__ int list[kCollect];  // by compact token; -1 for the tokens past the last
+  __shared__ int sums[kWaves];
+  __shared__ float tops[kWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const bool store = blockIdx.x == 0;
+  int64_t lab[kPer];
+  bool ok[kPer];
+  int mine = 0;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int m = kPer * tid + j;
+    lab[j] = m < M ? labels[m] : -1;
+    ok[j] = lab[j] >= 0 && lab[j] < V;
+    mine += ok[j];
+    list[m] = -1;
+  }
+  int inc = mine;  // inclusive sum over the wave
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(inc, d, 64);
+    if (lane >= d) inc += o;
+  }
+  if (lane == 63) sums[wave] = inc;
+  __syncthreads();
+  int at = inc - mine, n = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    at += w < wave ? sums[w] : 0;
+    n += sums[w];
+  }
+  float top = 0.0f;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int m = kPer * tid + j;
+    if (ok[j]) {
+      list[at] = m;
+      if (store) {
+        idx[at] = m;
+        label[at] = (int)lab[j];
+        if (lse) {
+          c_lse[at] = lse[m];
+          c_dloss[at] = dloss[m];
+          top = fmaxf(top, fabsf(dloss[m]));
+        }
+      }
+      ++at;
+    } else if (store && out_loss && m < M) {
+      out_loss[m] = 0.0f;
+      out_lse[m] = 0.0f;
+    }
+  }
+  if (store) {
+    if (tid == 0) *count = n;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+    if (lane == 0) tops[wave] = top;
+  }
+  __syncthreads();
+  if (store && lse && tid == 0) {
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) top = fmaxf(top, tops[w]);
+    *c_top = top;
+  }
+  const int pad = (n + 31) / 32 * 32;
+  const int64_t per = h / 8, rows = dH && M > pad ? M : pad;
+  for (int64_t e = (int64_t)blockIdx.x * 256 + tid; e < rows * per; e += (int64_t)gridDim.x * 256) {
+    const int i = (int)(e / per);
+    const int64_t c = e % per;
+    if (i < pad) {
+      const int m = list[i];
+      u32x4 v{0, 0, 0, 0};
+      if (m >= 0) v = *reinterpret_cast<const u32x4 *>(H + m * h + c * 8);
+      *reinterpret_cast<u32x4 *>(Hc + (int64_t)(i >> 5) * h * 32 + (i & 31) * 32 + (c >> 2) * 1024 + (c & 3) * 8) = v;
+    }
+    if (dH && i < M && (labels[i] < 0 || labels[i] >= V))
+      *reinterpret_cast<u32x4 *>(dH + i * h + c * 8) = u32x4{0, 0, 0, 0};
   }
 }
 
@@ -245,6 +336,27 @@ T *at(void *ws, size_t off) { return reinterpret_cast<T *>(reinterpret_cast<char
 
 unsigned grid4(int64_t M) { return (unsigned)(cdiv(M, 4) < 65536 ? cdiv(M, 4) : 65536); }
 
+// The compact tokens: list, their lse and dloss (backward), the copy of their rows.
+struct Compact {
+  int *count, *idx, *label;
+  float *lse, *dloss, *top;
+  uint16_t *H;
+};
+
+hipError_t collect(const LossArgs &a, const Compact &c, const float *lse, const float *dloss, float *out_loss,
+                   float *out_lse, uint16_t *dH, hipStream_t st) {
+  if (a.M <= kCollect) {
+    const int64_t groups = cdiv(cdiv(a.M, 32) * 32 * (a.h / 8), 256);
+    return launch(loss_collect_kernel, (unsigned)(groups < 1024 ? groups : 1024), 256, st, a.H, a.labels, a.M, a.h,
+                  a.V, c.count, c.idx, c.label, lse, dloss, c.lse, c.dloss, c.top, out_loss, out_lse, c.H, dH);
+  }
+  hipError_t e = launch(loss_select_kernel, 1, kSelThreads, st, a.labels, a.M, a.V, c.count, c.idx, c.label, lse,
+                        dloss, c.lse, c.dloss, c.top, out_loss, out_lse);
+  if (e != hipSuccess) return e;
+  return launch(loss_gather_kernel, grid4(a.M), 256, st, a.H, a.M, a.h, (const int *)c.count, (const int *)c.idx, c.H,
+                a.labels, a.V, dH);
+}
+
 }  // namespace
 
 bool loss_supported(int64_t M, int64_t h, int64_t V) {
@@ -260,12 +372,8 @@ hipError_t launch_loss_fwd(const LossArgs &a, float *loss, float *lse, void *ws,
   const LossLayout L = loss_layout(a.M, a.h, a.V, false);
   int *count = at<int>(ws, L.count), *idx = at<int>(ws, L.idx), *label = at<int>(ws, L.label);
   uint16_t *Hc = at<uint16_t>(ws, L.hc);
-  hipError_t e = launch(loss_select_kernel, 1, kSelThreads, st, a.labels, a.M, a.V, count, idx, label,
-                        (const float *)nullptr, (const float *)nullptr, (float *)nullptr, (float *)nullptr,
-                        (float *)nullptr, loss, lse);
-  if (e != hipSuccess) return e;
-  e = launch(loss_gather_kernel, grid4(a.M), 256, st, a.H, a.M, a.h, (const int *)count, (const int *)idx, Hc, a.labels,
-             a.V, (uint16_t *)nullptr);
+  hipError_t e = collect(a, Compact{count, idx, label, nullptr, nullptr, nullptr, Hc}, nullptr, nullptr, loss, lse,
+                         nullptr, st);
   if (e != hipSuccess) return e;
   LogitParams p{};
   p.W = a.W, p.H = Hc, p.count = count, p.label = label, p.h = a.h, p.v0 = 0, p.nvoc = a.V;
@@ -283,11 +391,7 @@ hipError_t launch_loss_bwd(const LossArgs &a, const float *lse, const float *dlo
   int *count = at<int>(ws, L.count), *idx = at<int>(ws, L.idx), *label = at<int>(ws, L.label);
   uint16_t *Hc = at<uint16_t>(ws, L.hc);
   float *c_lse = at<float>(ws, L.lse), *c_dl = at<float>(ws, L.dloss), *top = at<float>(ws, L.top);
-  hipError_t e = launch(loss_select_kernel, 1, kSelThreads, st, a.labels, a.M, a.V, count, idx, label, lse, dloss,
-                        c_lse, c_dl, top, (float *)nullptr, (float *)nullptr);
-  if (e != hipSuccess) return e;
-  e = launch(loss_gather_kernel, grid4(a.M), 256, st, a.H, a.M, a.h, (const int *)count, (const int *)idx, Hc, a.labels,
-             a.V, dH);
+  hipError_t e = collect(a, Compact{count, idx, label, c_lse, c_dl, top, Hc}, lse, dloss, nullptr, nullptr, dH, st);
   if (e != hipSuccess) return e;
   float *part = at<float>(ws, L.part);
   for (int64_t v0 = 0; v0 < a.V; v0 += L.piece) {
