@@ -36,7 +36,7 @@ struct LogitParams {
   float *zlab;          // [n] the label's logit
   // gradient: G = (exp(z - lse) - onehot) * (dloss / top)
   const float *lse, *dloss;  // [n]
-  const float *top;          // the largest |dloss| (device)
+  const float *top;          // the largest finite |dloss| (device)
   uint16_t *G;          // [n][piece], blocked, gblocks blocks per row; zero past nvoc up to
   int64_t gblocks;      // the next 256 and past n up to the next 32
 };

@@ -33,10 +33,17 @@ inline int64_t cdiv(int64_t x, int64_t m) { return (x + m - 1) / m; }
 
 constexpr int kSelThreads = 1024;
 
+// Infinities and NaN (an overflowed loss scale) do not count: they stay with their own
+// token's G instead of spoiling the common factor.
+QL_DEV float largest(float top, float v) {
+  const float a = fabsf(v);
+  return a < __builtin_inff() && a > top ? a : top;
+}
+
 }  // namespace
 
 // The tokens with a label in [0, V), in order: idx[i], label[i], and with `lse` the
-// compact lse and dloss and the largest |dloss|.  Tokens without one get loss = lse = 0 (forward).
+// compact lse and dloss and the largest finite |dloss|.  Tokens without one get loss = lse = 0 (forward).
 __global__ __launch_bounds__(kSelThreads) void loss_select_kernel(const int64_t *labels, int64_t M, int64_t V,
                                                                   int *count, int *idx, int *label,
                                                                   const float *lse, const float *dloss,
@@ -83,7 +90,7 @@ __global__ __launch_bounds__(kSelThreads) void loss_select_kernel(const int64_t 
         if (lse) {
           c_lse[at] = lse[m];
           c_dloss[at] = dloss[m];
-          top = fmaxf(top, fabsf(dloss[m]));
+          top = largest(top, dloss[m]);
         }
         ++at;
       } else if (out_loss && m < M) {
@@ -181,7 +188,7 @@ __global__ __launch_bounds__(256) void loss_collect_kernel(const uint16_t *H, co
         if (lse) {
           c_lse[at] = lse[m];
           c_dloss[at] = dloss[m];
-          top = fmaxf(top, fabsf(dloss[m]));
+          top = largest(top, dloss[m]);
         }
       }
       ++at;

@@ -204,7 +204,8 @@ __global__ __launch_bounds__(kThreads) void head_logits_kernel(LogitParams p) {
       const int col = wb + 32 * j + l32;
       const int64_t t = t0 + col;
       const bool live = t < n;
-      const float lse = live ? p.lse[t] : 0.0f, dl = live && top > 0.0f ? p.dloss[t] / top : 0.0f;
+      const float lse = live ? p.lse[t] : 0.0f;
+      const float raw = live ? p.dloss[t] : 0.0f, dl = top > 0.0f ? raw / top : raw;
       const int64_t lab = live ? (int64_t)p.label[t] - p.v0 - v0 : -1;
 #pragma unroll
       for (int i = 0; i < TA; ++i)

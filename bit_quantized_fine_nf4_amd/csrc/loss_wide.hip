@@ -263,7 +263,8 @@ __global__ __launch_bounds__(kThreads) void head_logits_wide_kernel(LogitParams 
       for (int j = 0; j < 4; ++j) {
         const int64_t t = t0 + wb + 32 * j + l32;
         const bool live = t < n;
-        const float lse = live ? p.lse[t] : 0.0f, dl = live && top > 0.0f ? p.dloss[t] / top : 0.0f;
+        const float lse = live ? p.lse[t] : 0.0f;
+        const float raw = live ? p.dloss[t] : 0.0f, dl = top > 0.0f ? raw / top : raw;
         const int lab = live ? p.label[t] - vbase : -1;
         // blocks of G: the wave's 32 tokens are one block row, tile ii one block (tokens past
         // the last: zero; the tile's rows are all there)

@@ -148,8 +148,9 @@ QL_DEV float wave_sum(float v) {
 
 constexpr int kMaxWaves = 16;
 
-// Sum over the workgroup's nw waves, in a fixed order; `red` has a float per wave that
-// nobody reads or writes until the barrier of the call after the next one.
+// Sum over the workgroup's nw waves, in a fixed order.  One barrier: the callers take the
+// four rows of `red` in turn, so a row is written again only after three more barriers,
+// when every wave has read it.
 QL_DEV float wg_sum(float v, float *red, int nw) {
   v = wave_sum(v);
   if (nw == 1) return v;

@@ -443,7 +443,8 @@ qlora_status_t qlora_norm_bwd(const uint16_t *dN, const void *dR_out, qlora_dtyp
  *  workspace: qlora_workspace_size(QLORA_OP_LOSS_FWD, M, h, V, 0) bytes.
  * qlora_loss_bwd  lse as the forward gave it; dloss [M] float32, the gradient of each
  *  token's loss (1 / count for the mean).  dH out, [M][h] bf16.  dW out, [V][h] bf16,
- *  or NULL: the head is frozen.  Outputs overlap nothing.
+ *  or NULL: the head is frozen.  Outputs overlap nothing.  A dloss that is not finite
+ *  makes its own token's dH not finite, and dW; the other tokens' dH are as without it.
  *  workspace: qlora_workspace_size(QLORA_OP_LOSS_BWD, M, h, V, 0) bytes.
  */
 qlora_status_t qlora_loss_fwd(const uint16_t *H, const uint16_t *W, const int64_t *labels, int64_t M, int64_t h,

@@ -108,7 +108,7 @@ def compare(got, H, W, labels, dl):
 
 SHAPES = [(1, 64, 1), (1, 64, 100), (1, 1024, 3001), (3, 128, 129), (16, 192, 1000), (31, 64, 128), (32, 64, 257),
           (33, 64, 300), (64, 256, 511), (65, 128, 512), (128, 64, 700), (129, 320, 513), (300, 256, 1000),
-          (257, 64, 5000), (513, 576, 770)]
+          (257, 64, 5000), (513, 576, 770), (1024, 64, 300), (1025, 64, 300)]
 
 
 @pytest.mark.parametrize("skip", ["none", "some", "most", "all"])
@@ -160,6 +160,29 @@ def test_pieces_of_the_vocabulary():
     compare(got, *t)
     again = run(*t)
     assert all(torch.equal(got[k], again[k]) for k in got)
+
+
+@pytest.mark.parametrize("M", [3, 100])
+def test_pieces_of_the_vocabulary_for_few_tokens(M):
+    """A vocabulary past one piece's 2^20 entries."""
+    t = [x.to(DEV) for x in problem(M, 64, (1 << 20) + 777, "none")]
+    compare(run(*t), *t)
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+@pytest.mark.parametrize("M", [20, 70, 300])
+def test_a_gradient_that_is_not_finite_stays_with_its_token(M, bad):
+    H, W, labels, dl = (x.to(DEV) for x in problem(M, 256, 600, "none"))
+    dl[7] = 0
+    _, lse = nf4.qlora_loss_fwd(H, W, labels)
+    live, ref = reference(H, W, labels, dl)
+    dl[7] = bad
+    dH, _ = nf4.qlora_loss_bwd(H, W, labels, lse, dl)
+    assert not torch.isfinite(dH[7]).any()
+    others = torch.arange(M, device=DEV) != 7
+    check("dH", dH[others], ref["dH"][0][others], ref["dH"][1][others])
+    alone, _ = nf4.qlora_loss_bwd(H, W, labels, lse, torch.full_like(dl, bad))
+    assert not torch.isfinite(alone).any()
 
 
 def test_gradient_by_differences():

@@ -3,7 +3,7 @@ against the float64 oracle (oracle/norm.py).
 
 Bounds, with u = 2^-24 (a float32 rounding) and H the output's own half step (2^-8 of
 the value for bf16, u for float32).  Each step of the chain rounds a few times: a sum
-over a row takes at most 16 additions per thread, 6 between lanes and 16 between waves,
+over a row takes at most 32 additions per thread, 6 between lanes and 16 between waves,
 its root and reciprocal 3 more and halve the sum's error, the products around it at most
 5: C = 64 roundings cover every chain.  They act on the magnitudes that enter:
   r     |R| + |alpha gate u|
@@ -104,7 +104,7 @@ def check_bwd(d, stats, alpha, got, M):
 
 
 SHAPES = [(1, 1), (1, 8192), (3, 7), (2, 64), (5, 511), (4, 512), (4, 513), (300, 1000), (3, 2047), (2, 2056),
-          (3, 4100), (7, 5003), (3, 8191), (2, 8193), (3, 16384), (2, 16381), (2500, 40)]
+          (3, 4100), (7, 5003), (1100, 5003), (700, 4099), (3, 8191), (300, 8185), (2, 8193), (3, 16384), (2, 16381), (2500, 40)]
 
 
 @pytest.mark.parametrize("rt", [BF, F32])
