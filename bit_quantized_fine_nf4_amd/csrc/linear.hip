@@ -41,6 +41,7 @@
 #include "gemm.h"
 #include "gemv.h"
 
+#include <algorithm>
 #include <type_traits>
 
 
@@ -388,23 +389,22 @@ struct GradProblem {
 
 constexpr int kGradTile = 128;  // values of i per workgroup
 
+constexpr int grad_lds(int NT) { return 2 * 64 * (kGradTile + 8) + 2 * 64 * (16 * NT + 8); }  // elements
+
 template <int NT>
-__global__ __launch_bounds__(256) void lora_grad_kernel(GradProblem pa, GradProblem pb, int rq, float s, int64_t M,
-                                                        int64_t mchunk, int64_t prows, float *__restrict__ part) {
+QL_DEV void grad_tile(uint16_t *lds, const GradProblem &pr, int64_t tile, int rq, float s, int64_t M, int64_t mchunk,
+                      int64_t prows, float *__restrict__ part) {
   constexpr int RP = NT * 16;
   constexpr int LP = kGradTile + 8;                   // P slab row stride (elements)
   constexpr int PCH = 64 * kGradTile / 8 / 256;       // 16-byte P chunks per thread per slab
   constexpr int QCH = (64 * RP / 8 + 255) / 256;      // 16-byte Q chunks per thread per slab (at most)
-  __shared__ __attribute__((aligned(16))) uint16_t Ps[2][64 * LP];
+  uint16_t (*Ps)[64 * LP] = reinterpret_cast<uint16_t (*)[64 * LP]>(lds);
   // Q slab: rows padded to LQ when ldq is a multiple of 8 (transposing reads), else
   // kept as it is in memory (ldq-element rows, 2-byte gathers)
   constexpr int LQ = RP + 8;
-  __shared__ __attribute__((aligned(16))) uint16_t Qs[2][64 * LQ];
+  uint16_t (*Qs)[64 * LQ] = reinterpret_cast<uint16_t (*)[64 * LQ]>(lds + 2 * 64 * LP);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int g = lane >> 4, c16 = lane & 15;
-  const bool second = blockIdx.x >= pa.tiles;
-  const GradProblem &pr = second ? pb : pa;
-  const int64_t tile = second ? blockIdx.x - pa.tiles : blockIdx.x;
   const int64_t i0 = tile * kGradTile;
   const int64_t ms = (int64_t)blockIdx.y * mchunk;
   const int64_t me = ms + mchunk < M ? ms + mchunk : M;
@@ -550,6 +550,14 @@ __global__ __launch_bounds__(256) void lora_grad_kernel(GradProblem pa, GradProb
         const int q = t * 16 + c16;
         if (i < pr.I && q < rq) pr.out[pr.trans ? (int64_t)q * pr.I + i : i * rq + q] = s * acc[a][t][v];
       }
+}
+
+template <int NT>
+__global__ __launch_bounds__(256) void lora_grad_kernel(GradProblem pa, GradProblem pb, int rq, float s, int64_t M,
+                                                        int64_t mchunk, int64_t prows, float *__restrict__ part) {
+  __shared__ __attribute__((aligned(16))) uint16_t lds[grad_lds(NT)];
+  const bool second = blockIdx.x >= pa.tiles;
+  grad_tile<NT>(lds, second ? pb : pa, second ? blockIdx.x - pa.tiles : blockIdx.x, rq, s, M, mchunk, prows, part);
 }
 
 // Sum of the adapter gradients' token splits, in split order, scaled by s.  A
@@ -927,14 +935,16 @@ __global__ __launch_bounds__(kP16Threads) void lora_gradp_kernel(GradProblem pa,
 // ---------------------------------------------------------------------------
 // dL1 = s·(keep ⊙ X)^T·U with dropout on the adapter's input.  A workgroup owns 128
 // values of i (columns of X), every rank column and a token range, walked in 64-token
-// slabs, as lora_grad_kernel does: X comes back from LDS through transposing reads.
+// slabs, as grad_tile does: X comes back from LDS through transposing reads.
 // X's pieces are masked on their way into LDS, one generator call per 16-byte piece and
 // every piece in one workgroup only.  U comes as the float32 sums of the rank-r product
 // and is split into three bf16 parts (U = hi + mid + lo to 2^-26), each a product of its
 // own on the same accumulators: one bf16 U alone would leave dL1, a float32 result, with
-// 2^-9 errors.  The product is bound by reading X, not by the matrix cores.  With one
-// token split the kernel scales by s and stores; otherwise lora_grad_reduce_kernel adds
-// the splits in order.
+// 2^-9 errors.  The product is bound by reading X, not by the matrix cores.
+// The launch's other workgroups are dL2's: neither fills the chip alone, and the two
+// share one reduce launch (2048 tokens, 4096 x 4096, r = 16: 10.5 + 4.9 us, apart 8.4 +
+// 5.0 and 8.9; 8192 x 22016, r = 64: 44.5 + 7.2 us, apart 19.6 + 4.9 and 22.6 + 5.7).
+// Token splits are made for 512 workgroups, two to a compute unit (for 256: 12.0, 51.8 us).
 // ---------------------------------------------------------------------------
 QL_DEV void split3(float x, float &hi, float &mid, float &lo) {
   hi = bf16_lo(pack_bf16x2(x, 0.0f));
@@ -942,16 +952,17 @@ QL_DEV void split3(float x, float &hi, float &mid, float &lo) {
   lo = (x - hi) - mid;
 }
 
+constexpr int drop_lds(int NT) { return 2 * 64 * (kGradTile + 8) + 3 * 64 * (16 * NT + 8); }  // elements
+
 template <int NT>
-__global__ __launch_bounds__(256) void drop_grad_kernel(GradProblem pr, const float *U, DropState drop, int rq, float s,
-                                                        int64_t M, int64_t mchunk, int64_t prows,
-                                                        float *__restrict__ part) {
+QL_DEV void drop_tile(uint16_t *lds, const GradProblem &pr, const float *U, const DropState &drop, int rq, float s,
+                      int64_t M, int64_t mchunk, int64_t prows, float *__restrict__ part) {
   constexpr int RP = NT * 16;
   constexpr int LP = kGradTile + 8, LQ = RP + 8;
   constexpr int PCH = 64 * kGradTile / 8 / 256;  // 16-byte pieces of X per thread and slab (4)
   constexpr int QCH = 64 * RP / 4 / 256;         // 16-byte pieces of U per thread and slab (NT)
-  __shared__ __attribute__((aligned(16))) uint16_t Ps[2][64 * LP];
-  __shared__ __attribute__((aligned(16))) uint16_t Qs[3][64 * LQ];
+  uint16_t (*Ps)[64 * LP] = reinterpret_cast<uint16_t (*)[64 * LP]>(lds);
+  uint16_t (*Qs)[64 * LQ] = reinterpret_cast<uint16_t (*)[64 * LQ]>(lds + 2 * 64 * LP);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int g = lane >> 4, c16 = lane & 15;
   const int64_t i0 = (int64_t)blockIdx.x * kGradTile;
@@ -1072,10 +1083,10 @@ struct Split {
 // offsets and its view is capped below 2^31 bytes.
 int64_t grad_chunk_cap(int64_t ld) { return ((int64_t)0x7FFFFFF0 / (2 * ld)) / 64 * 64; }
 
-Split grad_split(int64_t M, int64_t I, int64_t maxld) {
-  // about kTargetGroups workgroups: more token splits cost more in partial sums than they save
+Split grad_split(int64_t M, int64_t I, int64_t maxld, int groups = kTargetGroups) {
+  // about `groups` workgroups: more token splits cost more in partial sums than they save
   const int64_t it = cdiv(I, kGradTile);
-  int64_t S = cdiv(kTargetGroups, it);
+  int64_t S = cdiv(groups, it);
   const int64_t msteps = cdiv(M, 64);
   S = S < 1 ? 1 : S;
   S = S > msteps ? msteps : S;
@@ -1167,6 +1178,15 @@ BwdLayout bwd_layout(int64_t M, int64_t h, int64_t o, int r) {
 
 template <typename T>
 T *at(void *ws, size_t off) { return reinterpret_cast<T *>(reinterpret_cast<char *>(ws) + off); }
+
+template <int NT>
+__global__ __launch_bounds__(256) void drop_grad_kernel(GradProblem pa, GradProblem pb, const float *U, DropState drop,
+                                                        int rq, float s, int64_t M, int64_t mchunk, int64_t prows,
+                                                        float *__restrict__ part) {
+  __shared__ __attribute__((aligned(16))) uint16_t lds[drop_lds(NT)];
+  if (blockIdx.x < pa.tiles) drop_tile<NT>(lds, pa, U, drop, rq, s, M, mchunk, prows, part);
+  else grad_tile<NT>(lds, pb, blockIdx.x - pa.tiles, rq, s, M, mchunk, prows, part);
+}
 
 // DROP: dropout on the forward's X (kn)
 template <bool DROP = false>
@@ -1703,8 +1723,8 @@ namespace {
 
 struct DropLayout {
   int RP16, RP64, dxc;
-  Split s1, s2;  // token splits of dL1 and dL2
-  size_t off_u, off_su, off_l1p, off_g1, off_g2, off_up, off_dxp, total;
+  Split gs;  // token splits of dL1 and dL2
+  size_t off_u, off_su, off_l1p, off_g, off_up, off_dxp, total;
 };
 
 DropLayout drop_layout(int64_t M, int64_t h, int64_t o, int r) {
@@ -1718,30 +1738,28 @@ DropLayout drop_layout(int64_t M, int64_t h, int64_t o, int r) {
     L.off_dxp = take((size_t)L.dxc * M * h * 4);
   }
   // a split's rows of X, U (float32), dY and T stay within 32-bit offsets
-  L.s1 = grad_split(M, h, h > 2 * L.RP16 ? h : 2 * L.RP16);
-  L.s2 = grad_split(M, o, o > L.RP16 ? o : L.RP16);
+  L.gs = grad_split(M, h + o, std::max({h, o, (int64_t)2 * L.RP16}), 2 * kTargetGroups);
   L.off_u = take((size_t)M * L.RP16 * 4);
   L.off_su = take((size_t)M * L.RP64 * 2);
   L.off_l1p = take((size_t)h * L.RP64 * 2);
-  L.off_g1 = take(L.s1.S > 1 ? (size_t)L.s1.S * h * L.RP16 * 4 : 0);
-  L.off_g2 = take(grad_one_pass(M, 0, o, L.RP16) ? 0 : (size_t)L.s2.S * o * L.RP16 * 4);
+  L.off_g = take(L.gs.S > 1 ? (size_t)L.gs.S * (h + o) * L.RP16 * 4 : 0);
   L.off_up = take(rank_partial_bytes(M, o, L.RP16));
   L.total = off;
   return L;
 }
 
-hipError_t drop_grad(const GradProblem &pr, const float *U, const DropState &d, int r, float s, int64_t M, int RP16,
-                     const Split &sp, float *part, hipStream_t st) {
-  const dim3 grid((unsigned)pr.tiles, (unsigned)sp.S);
-  const GradProblem none{};
+hipError_t drop_grad(const GradProblem &pa, const GradProblem &pb, const float *U, const DropState &d, int r, float s,
+                     int64_t M, int RP16, const Split &sp, float *part, hipStream_t st) {
+  const int64_t prows = pa.I + pb.I;
+  const dim3 grid((unsigned)(pa.tiles + pb.tiles), (unsigned)sp.S);
   hipError_t e = hipErrorInvalidValue;
   switch (RP16 / 16) {
-#define QL_DG(NT)                                                                                            \
-  case NT:                                                                                                   \
-    e = launch(drop_grad_kernel<NT>, grid, 256, st, pr, U, d, r, s, M, sp.chunk, pr.I, part);                \
-    if (e == hipSuccess && sp.S > 1)                                                                         \
-      e = launch(lora_grad_reduce_kernel<NT * 16>, (unsigned)(pr.I / kGradRedRows), 256, st, pr, none, r, s, \
-                 sp.S, pr.I, (const float *)part);                                                           \
+#define QL_DG(NT)                                                                                                \
+  case NT:                                                                                                       \
+    e = launch(drop_grad_kernel<NT>, grid, 256, st, pa, pb, U, d, r, s, M, sp.chunk, prows, part);               \
+    if (e == hipSuccess && sp.S > 1)                                                                             \
+      e = launch(lora_grad_reduce_kernel<NT * 16>, (unsigned)(prows / kGradRedRows), 256, st, pa, pb, r, s, sp.S, \
+                 prows, (const float *)part);                                                                    \
     break;
     QL_DG(1) QL_DG(2) QL_DG(3) QL_DG(4) QL_DG(5) QL_DG(6) QL_DG(7) QL_DG(8)
 #undef QL_DG
@@ -1760,7 +1778,7 @@ size_t linear_drop_workspace(int64_t M, int64_t h, int64_t o, int r) {
 bool linear_drop_supported(int64_t M, int64_t h, int64_t o, int r) {
   if (r == 0) return true;
   const DropLayout L = drop_layout(M, h, o, r);
-  return L.s1.S <= 65535 && L.s2.S <= 65535;
+  return L.gs.S <= 65535;
 }
 
 hipError_t launch_linear_fwd_drop(const LinearArgs &a, const DropState &d, const uint16_t *X, const uint16_t *L1,
@@ -1784,10 +1802,8 @@ hipError_t launch_linear_bwd_drop(const LinearArgs &a, const DropState &d, const
   hipError_t e = rank_r(rp, false, L.RP16, at<float>(ws, L.off_up), st);
   if (e != hipSuccess) return e;
   const GradProblem g1{X, a.h, a.h, nullptr, 0, dL1, false, cdiv(a.h, kGradTile), 0};
-  const GradProblem g2{dY, a.o, a.o, T, a.r, dL2, true, cdiv(a.o, kGradTile), 0};
-  e = drop_grad(g1, U, d, a.r, a.s, a.M, L.RP16, L.s1, at<float>(ws, L.off_g1), st);
-  if (e != hipSuccess) return e;
-  e = lora_grad(GradProblem{}, g2, a.r, a.s, a.M, L.RP16, L.s2, at<float>(ws, L.off_g2), st);
+  const GradProblem g2{dY, a.o, a.o, T, a.r, dL2, true, cdiv(a.o, kGradTile), a.h};
+  e = drop_grad(g1, g2, U, d, a.r, a.s, a.M, L.RP16, L.gs, at<float>(ws, L.off_g), st);
   if (e != hipSuccess) return e;
   if (a.M <= 16) {
     GvdParams vp{};
