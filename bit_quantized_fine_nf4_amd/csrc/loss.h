@@ -34,12 +34,18 @@ struct LogitParams {
   f32x2 *part;          // [ceil(nvoc / 128), even for 256-row tiles][ldp]
   int64_t ldp;
   float *zlab;          // [n] the label's logit
+  // statistics of at most kFewTokens tokens without a compact copy (labels set): H is all
+  // tokens' hidden states, [M][h] as they are
+  const int64_t *labels;  // [M]
+  int64_t M;
   // gradient: G = (exp(z - lse) - onehot) * (dloss / top)
   const float *lse, *dloss;  // [n]
   const float *top;          // the largest finite |dloss| (device)
   uint16_t *G;          // [n][piece], blocked, gblocks blocks per row; zero past nvoc up to
   int64_t gblocks;      // the next 256 and past n up to the next 32
 };
+constexpr int kFewTokens = 32;
+hipError_t launch_logit_stats_few(LogitParams &p, hipStream_t st);
 // max_tokens bounds n and chooses the tiles
 hipError_t launch_logit_stats(LogitParams &p, int64_t max_tokens, hipStream_t st);
 hipError_t launch_logit_grad(LogitParams &p, int64_t max_tokens, hipStream_t st);

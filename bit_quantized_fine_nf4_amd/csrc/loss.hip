@@ -17,10 +17,11 @@
 // others are first gathered into a compact copy of H, so such tokens cost no products
 // and whatever their rows hold (NaN included) reaches nothing.  Their number is known
 // on the GPU only: launches are sized for all M tokens and the surplus workgroups leave.
+// (The forward of at most 32 tokens, one tile either way, takes H as it is.)
 //
 // Kernels: loss_select_kernel (one workgroup: the compact list), loss_gather_kernel
 // (the copy; zeroes the skipped rows of dH), both as loss_collect_kernel where the tokens
-// are few, the products of loss_gemm.hip,
+// are few, the products of loss_gemm.hip (few tokens) and loss_wide.hip,
 // loss_finish_kernel (lse and loss from the tiles' statistics), loss_dh_kernel (sums
 // dH's partials and rounds).  Everything is added in a fixed order: no atomics.
 
@@ -225,19 +226,31 @@ __global__ __launch_bounds__(256) void loss_collect_kernel(const uint16_t *H, co
   }
 }
 
-// lse and loss of compact token i from the tiles' (max, sum).  One wave per token.
+// lse and loss of token i from the tiles' (max, sum): compact tokens, or with `labels` all
+// M, of which those without a label in [0, V) get 0.  One wave per token.
 __global__ __launch_bounds__(256) void loss_finish_kernel(const f32x2 *part, int64_t ldp, int tiles, const int *count,
-                                                          const int *idx, const float *zlab, float *loss, float *lse) {
+                                                          const int *idx, const int64_t *labels, int64_t M, int64_t V,
+                                                          const float *zlab, float *loss, float *lse) {
+  constexpr int kAhead = 8;  // tiles in flight per lane
   const int lane = threadIdx.x & 63;
   const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (i >= *count) return;
+  if (i >= (labels ? M : *count)) return;
+  const int64_t token = labels ? i : idx[i];
+  const bool live = !labels || (labels[i] >= 0 && labels[i] < V);
+  const float z = live ? zlab[i] : 0.0f;  // (written for these tokens only)
   float mx = -__builtin_inff(), s = 0.0f;
-  for (int t = lane; t < tiles; t += 64) {
-    const f32x2 a = part[(int64_t)t * ldp + i];
-    if (a[1] == 0.0f) continue;  // no rows of the vocabulary
-    const float m = fmaxf(mx, a[0]);
-    s = s * __expf(mx - m) + a[1] * __expf(a[0] - m);
-    mx = m;
+  for (int t0 = lane; t0 < tiles; t0 += 64 * kAhead) {
+    f32x2 a[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      a[k] = t0 + 64 * k < tiles ? part[(int64_t)(t0 + 64 * k) * ldp + i] : f32x2{0.0f, 0.0f};
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (a[k][1] == 0.0f) continue;  // no rows of the vocabulary
+      const float m = fmaxf(mx, a[k][0]);
+      s = s * __expf(mx - m) + a[k][1] * __expf(a[k][0] - m);
+      mx = m;
+    }
   }
   float top = mx;
 #pragma unroll
@@ -247,8 +260,8 @@ __global__ __launch_bounds__(256) void loss_finish_kernel(const f32x2 *part, int
   for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d, 64);
   if (lane == 0) {
     const float l = top + logf(s);
-    lse[idx[i]] = l;
-    loss[idx[i]] = l - zlab[i];
+    lse[token] = live ? l : 0.0f;
+    loss[token] = live ? l - z : 0.0f;
   }
 }
 
@@ -379,17 +392,22 @@ hipError_t launch_loss_fwd(const LossArgs &a, float *loss, float *lse, void *ws,
   const LossLayout L = loss_layout(a.M, a.h, a.V, false);
   int *count = at<int>(ws, L.count), *idx = at<int>(ws, L.idx), *label = at<int>(ws, L.label);
   uint16_t *Hc = at<uint16_t>(ws, L.hc);
-  hipError_t e = collect(a, Compact{count, idx, label, nullptr, nullptr, nullptr, Hc}, nullptr, nullptr, loss, lse,
-                         nullptr, st);
-  if (e != hipSuccess) return e;
   LogitParams p{};
   p.W = a.W, p.H = Hc, p.count = count, p.label = label, p.h = a.h, p.v0 = 0, p.nvoc = a.V;
   p.part = at<f32x2>(ws, L.stat), p.ldp = a.M, p.zlab = at<float>(ws, L.zlab);
-  e = launch_logit_stats(p, a.M, st);
+  hipError_t e;
+  if (a.M <= kFewTokens) {
+    p.H = a.H, p.labels = a.labels, p.M = a.M;
+    e = launch_logit_stats_few(p, st);
+  } else {
+    e = collect(a, Compact{count, idx, label, nullptr, nullptr, nullptr, Hc}, nullptr, nullptr, loss, lse, nullptr, st);
+    if (e != hipSuccess) return e;
+    e = launch_logit_stats(p, a.M, st);
+  }
   if (e != hipSuccess) return e;
   return launch(loss_finish_kernel, (unsigned)cdiv(a.M, 4), 256, st, (const f32x2 *)p.part, p.ldp,
-                logit_parts(a.M, a.h, a.V),
-                (const int *)count, (const int *)idx, (const float *)p.zlab, loss, lse);
+                logit_parts(a.M, a.h, a.V), (const int *)count, (const int *)idx, p.labels, a.M, a.V,
+                (const float *)p.zlab, loss, lse);
 }
 
 hipError_t launch_loss_bwd(const LossArgs &a, const float *lse, const float *dloss, uint16_t *dH, uint16_t *dW,

@@ -128,7 +128,11 @@ constexpr int lmax(int a, int b) { return a > b ? a : b; }
 // GRAD false: part[tile][token] = (max, sum of exp(z - max)) over the tile's rows, and
 // zlab of the tokens whose label is among them.
 // GRAD true: G[token][v] = bf16((exp(z - lse) - [v is the label]) * (dloss / top)).
-template <int BV, int BT, int WV, int SA, int SB, int BK, bool GRAD>
+// FEW (statistics only): the tokens are at most BT, one tile with or without those that
+// carry no loss, so they come straight from H and no list is made.  (A token is a column
+// of the product: what the others' rows hold stays in their own statistics, which nobody
+// reads.)  16 x 4096 x 32000: 63 us in all, with a list and a copy of the rows first 69.
+template <int BV, int BT, int WV, int SA, int SB, int BK, bool GRAD, bool FEW>
 __global__ __launch_bounds__(kThreads) void head_logits_kernel(LogitParams p) {
   constexpr int WT = 4 / WV, TA = BV / WV / 32, TB = BT / WT / 32;
   constexpr int kRing = (SA * BV + SB * BT) * BK;  // elements
@@ -138,7 +142,10 @@ __global__ __launch_bounds__(kThreads) void head_logits_kernel(LogitParams p) {
   uint16_t *ring = reinterpret_cast<uint16_t *>(lds);
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 5, l32 = lane & 31;
-  const int n = *p.count;
+  static_assert(!FEW || (!GRAD && BT == kFewTokens), "one tile of tokens");
+  const int n = FEW ? (int)p.M : *p.count;
+  int64_t few_label = -1;
+  if constexpr (FEW) few_label = l32 < n ? p.labels[l32] : -1;
   const int tiles_t = (n + BT - 1) / BT;
   if ((int64_t)blockIdx.x >= (int64_t)tiles_t * p.tiles_v) return;
   int tv, tt;
@@ -146,11 +153,11 @@ __global__ __launch_bounds__(kThreads) void head_logits_kernel(LogitParams p) {
   const int64_t v0 = (int64_t)tv * BV, t0 = (int64_t)tt * BT;
   const int wa = wv / WT * (BV / WV), wb = wv % WT * (BT / WT);  // the wave's first row and column
   RowOperand<BV, BK> A;
-  BlockRows<BT, BK> B;
+  std::conditional_t<FEW, RowOperand<BT, BK>, BlockRows<BT, BK>> B;
   A.init(p.h, lane, wv, wa);
-  B.init(p.h * 64, lane, wv, wb);
+  B.init(FEW ? p.h : p.h * 64, lane, wv, wb);
   const u32x4 ra = lrsrc(p.W + v0 * p.h, (p.nvoc - v0) * p.h * 2);
-  const u32x4 rb = lrsrc(p.H + t0 * p.h, ((n + 31) / 32 * 32 - t0) * p.h * 2);
+  const u32x4 rb = lrsrc(p.H + t0 * p.h, ((FEW ? n : (n + 31) / 32 * 32) - t0) * p.h * 2);
   f32x16 acc[TA][TB];
   clear(acc);
   product<SA, SB, BK, TA, TB>(A, B, ra, rb, ring, (int)(p.h / BK), lane, wv, acc);
@@ -162,7 +169,7 @@ __global__ __launch_bounds__(kThreads) void head_logits_kernel(LogitParams p) {
     for (int j = 0; j < TB; ++j) {
       const int64_t t = t0 + wb + 32 * j + l32;
       // the label's row in this tile (none: a row that no lane has)
-      const int64_t lab = t < n ? (int64_t)p.label[t] - p.v0 - v0 : -1;
+      const int64_t lab = FEW ? few_label - v0 : t < n ? (int64_t)p.label[t] - p.v0 - v0 : -1;
       float mx = -__builtin_inff();
 #pragma unroll
       for (int i = 0; i < TA; ++i)
@@ -292,15 +299,20 @@ hipError_t logits(LogitParams &p, int64_t max_tokens, hipStream_t st) {
   if (logits_wide(max_tokens, p.h)) return launch_logit_wide(p, GRAD, st);
   // G is written (zero past the piece) up to a multiple of 256
   p.tiles_v = GRAD ? 2 * (int)cdiv(p.nvoc, 256) : (int)cdiv(p.nvoc, 128);
-  if (max_tokens <= 32)
-    return launch(head_logits_kernel<128, 32, 4, 4, 4, 64, GRAD>, (unsigned)p.tiles_v, kThreads, st, p);
-  return launch(head_logits_kernel<128, 128, 2, 3, 2, 64, GRAD>, (unsigned)(p.tiles_v * cdiv(max_tokens, 128)),
+  if constexpr (GRAD)
+    if (max_tokens <= kFewTokens)
+      return launch(head_logits_kernel<128, 32, 4, 4, 4, 64, true, false>, (unsigned)p.tiles_v, kThreads, st, p);
+  return launch(head_logits_kernel<128, 128, 2, 3, 2, 64, GRAD, false>, (unsigned)(p.tiles_v * cdiv(max_tokens, 128)),
                 kThreads, st, p);
 }
 }  // namespace
 
 hipError_t launch_logit_stats(LogitParams &p, int64_t max_tokens, hipStream_t st) {
   return logits<false>(p, max_tokens, st);
+}
+hipError_t launch_logit_stats_few(LogitParams &p, hipStream_t st) {
+  p.tiles_v = (int)cdiv(p.nvoc, 128);
+  return launch(head_logits_kernel<128, 32, 4, 4, 4, 64, false, true>, (unsigned)p.tiles_v, kThreads, st, p);
 }
 hipError_t launch_logit_grad(LogitParams &p, int64_t max_tokens, hipStream_t st) {
   return logits<true>(p, max_tokens, st);
