@@ -281,7 +281,22 @@ __global__ __launch_bounds__(256) void loss_dh_kernel(const float *part, int spl
     const int64_t i = e / per, c = e % per * 8;
     const float *src = part + i * h + c;
     f32x4 a = *reinterpret_cast<const f32x4 *>(src), b = *reinterpret_cast<const f32x4 *>(src + 4);
-    for (int s = 1; s < splits; ++s) {
+    int s = 1;
+    for (; s + 7 < splits; s += 8) {  // eight splits' loads in flight, added in order
+      f32x4 u[8], w[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float *q = src + (int64_t)(s + k) * stride;
+        u[k] = *reinterpret_cast<const f32x4 *>(q);
+        w[k] = *reinterpret_cast<const f32x4 *>(q + 4);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        a += u[k];
+        b += w[k];
+      }
+    }
+    for (; s < splits; ++s) {
       const float *q = src + (int64_t)s * stride;
       a += *reinterpret_cast<const f32x4 *>(q);
       b += *reinterpret_cast<const f32x4 *>(q + 4);
