@@ -50,7 +50,7 @@ hipError_t launch_logit_stats_few(LogitParams &p, hipStream_t st);
 hipError_t launch_logit_stats(LogitParams &p, int64_t max_tokens, hipStream_t st);
 hipError_t launch_logit_grad(LogitParams &p, int64_t max_tokens, hipStream_t st);
 hipError_t launch_logit_wide(LogitParams &p, bool grad, hipStream_t st);  // 256 x 256 tiles
-bool logits_wide(int64_t max_tokens, int64_t h);
+bool logits_wide(int64_t max_tokens, int64_t h, int64_t nvoc);
 int logit_parts(int64_t max_tokens, int64_t h, int64_t V);  // rows of part
 
 struct HeadGradParams {

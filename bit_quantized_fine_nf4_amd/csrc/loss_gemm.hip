@@ -286,17 +286,23 @@ namespace {
 inline int64_t cdiv(int64_t x, int64_t m) { return (x + m - 1) / m; }
 }  // namespace
 
-// Tokens from which the 256 x 256 tiles are used: the statistics of 129 tokens fill half
-// of such a tile, 128 fill one of 128 x 128.  They need h of three 64-deep stages.
-bool logits_wide(int64_t max_tokens, int64_t h) { return max_tokens > 128 && h >= 192; }
+// Whether the logits run on 256 x 256 tiles, one persistent workgroup per compute unit, or
+// on 128 x 128, two workgroups per compute unit: the larger ones once the smaller ones take
+// a second round (more than 512), before which they would leave compute units idle (4096
+// values, 256 tokens: 10000 words 92 against 46 us, 32000 words 101 against 93, 50257 words,
+// 786 small tiles, 136 against 164).  Up to 128 tokens half of every larger tile would be
+// empty; and they need h of three 64-deep stages.
+bool logits_wide(int64_t max_tokens, int64_t h, int64_t nvoc) {
+  return max_tokens > 128 && h >= 192 && cdiv(max_tokens, 128) * cdiv(nvoc, 128) > 512;
+}
 int logit_parts(int64_t max_tokens, int64_t h, int64_t V) {
-  return logits_wide(max_tokens, h) ? 2 * (int)cdiv(V, 256) : (int)cdiv(V, 128);
+  return logits_wide(max_tokens, h, V) ? 2 * (int)cdiv(V, 256) : (int)cdiv(V, 128);
 }
 
 namespace {
 template <bool GRAD>
 hipError_t logits(LogitParams &p, int64_t max_tokens, hipStream_t st) {
-  if (logits_wide(max_tokens, p.h)) return launch_logit_wide(p, GRAD, st);
+  if (logits_wide(max_tokens, p.h, p.nvoc)) return launch_logit_wide(p, GRAD, st);
   // G is written (zero past the piece) up to a multiple of 256
   p.tiles_v = GRAD ? 2 * (int)cdiv(p.nvoc, 256) : (int)cdiv(p.nvoc, 128);
   if constexpr (GRAD)
