@@ -647,27 +647,27 @@ __global__ __launch_bounds__(kThreads) void nf4_gemm_wide_dx_kernel(GemmParams p
       const auto rB2 = wrsrc(p.B2 + n0 * p.ldb2, nrows * p.ldb2 * 2);
       uint16_t *a2 = ring;
       for (int k2 = 0; k2 < p.ksteps2; ++k2) {
-  #pragma unroll
+#pragma unroll
         for (int u = 0; u < 8; ++u) {
           const int ch = tid + kThreads * u, r = ch >> 3, lc = ch & 7;
           const u32x4 v = wload128(rA2, (int)((r * p.lda2 + lc * 8) * 2), k2 * kBK * 2);
           *reinterpret_cast<u32x4 *>(a2 + r * kBK + ((lc ^ a_swz(r)) << 3)) = v;
         }
         u32x4 b2[kTN][4];
-  #pragma unroll
+#pragma unroll
         for (int j = 0; j < kTN; ++j)
-  #pragma unroll
+#pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             b2[j][kk] = wload128(rB2, (int)(((64 * wv + 32 * j + (l32 ^ 1)) * p.ldb2 + 32 * g + 8 * kk) * 2),
                                  k2 * kBK * 2);
         __syncthreads();
-  #pragma unroll
+#pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
           u32x4 a[kTM];
           read_a(0, kk, a);
-  #pragma unroll
+#pragma unroll
           for (int i = 0; i < kTM; ++i)
-  #pragma unroll
+#pragma unroll
             for (int j = 0; j < kTN; ++j) acc[i][j] = wmfma(a[i], b2[j][kk], acc[i][j]);
         }
         __syncthreads();
