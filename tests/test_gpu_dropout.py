@@ -132,7 +132,7 @@ def run_case(M, h, o, r, p, s=2.0, codebook="nf4", seed=3, offset=2 ** 32 - 5):
 
 CASES = [(1, 64, 64, 1), (2, 192, 128, 8), (9, 128, 640, 5), (16, 1024, 320, 64), (17, 64, 192, 16), (40, 320, 64, 17),
          (64, 128, 128, 100), (65, 576, 256, 128), (129, 192, 448, 33), (300, 256, 192, 7), (700, 512, 384, 64),
-         (2100, 128, 64, 16), (200, 20480, 64, 8), (300, 30720, 64, 5), (257, 30720, 192, 70), (520, 15424, 448, 16)]
+         (2100, 128, 64, 16), (200, 20480, 64, 8), (300, 30848, 64, 5), (257, 30848, 192, 70), (520, 15424, 448, 16)]
 
 
 @pytest.mark.parametrize("p", [0.05, 0.5])
@@ -148,7 +148,7 @@ def test_linear_codebooks(codebook):
     run_case(5, 128, 192, 16, 0.1, codebook=codebook)
 
 
-@pytest.mark.parametrize("M,h,o,r", [(5, 128, 192, 16), (70, 128, 256, 24), (300, 30720, 64, 8)])
+@pytest.mark.parametrize("M,h,o,r", [(5, 128, 192, 16), (70, 128, 256, 24), (300, 30848, 64, 8)])
 def test_no_dropout_is_the_plain_linear(M, h, o, r):
     Wq, d, rng, Y, T, _ = run_case(M, h, o, r, 0.0)
     pY, pT = nf4.qlora_linear_fwd(Wq, *d, 2.0)
