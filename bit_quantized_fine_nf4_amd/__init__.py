@@ -120,12 +120,10 @@ def _dev_check(*ts):
 
 def _want(name: str, t: Optional[torch.Tensor], dtype, shape: tuple, device):
     """Refuses a tensor that the C call would misread: its type, shape, layout or device."""
-    if t is None:
-        return
-    if t.get_device() != device.index or not t.is_contiguous():  # (a CPU tensor: -1 and None)
-        raise ValueError(f"{name} must be contiguous and on {device}")
-    if t.dtype is not dtype or t.shape != shape:
-        raise ValueError(f"{name} is {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if t is not None and (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
+                          or t.get_device() != device.index):  # (a CPU tensor: -1 and None)
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def _at(t: Optional[torch.Tensor]):
@@ -474,12 +472,16 @@ def qlora_norm_fwd(R: torch.Tensor, Y: Optional[torch.Tensor] = None, w_pre: Opt
         rstd_pre = torch.empty(M, dtype=torch.float32, device=dev) if rstd_pre is None else rstd_pre
     if w_post is not None and rstd_post is None:
         rstd_post = torch.empty(M, dtype=torch.float32, device=dev)
-    for name, t, dtype, shape in (("R", R, R.dtype, (M, h)), ("R_out", R_out, R.dtype, (M, h)),
-                                  ("Y", Y, torch.bfloat16, (M, h)), ("N", N, torch.bfloat16, (M, h)),
-                                  ("w_pre", w_pre, torch.float32, (h,)), ("w_post", w_post, torch.float32, (h,)),
-                                  ("gate", gate, torch.float32, (h,)), ("rstd_pre", rstd_pre, torch.float32, (M,)),
-                                  ("rstd_post", rstd_post, torch.float32, (M,))):
-        _want(name, t, dtype, shape, dev)
+    rows, cols, one, bf, f32 = (M, h), (h,), (M,), torch.bfloat16, torch.float32
+    _want("R", R, R.dtype, rows, dev)
+    _want("R_out", R_out, R.dtype, rows, dev)
+    _want("Y", Y, bf, rows, dev)
+    _want("N", N, bf, rows, dev)
+    _want("w_pre", w_pre, f32, cols, dev)
+    _want("w_post", w_post, f32, cols, dev)
+    _want("gate", gate, f32, cols, dev)
+    _want("rstd_pre", rstd_pre, f32, one, dev)
+    _want("rstd_post", rstd_post, f32, one, dev)
     _call(dev, "qlora_norm_fwd", _at(R), dt, _at(Y), _at(w_post), _at(gate), float(alpha), _at(w_pre),
           float(eps), M, h, _at(R_out), _at(N), _at(rstd_post), _at(rstd_pre))
     return R_out, N, rstd_pre, rstd_post

@@ -12,6 +12,10 @@
 //   dY = du, or  rstd_post * (du * w_post - y * mean(du * w_post * y))
 //   dw_pre = sum dN * x,  dw_post = sum du * y,  dgate = sum alpha * dr * u
 //
+// The second mean needs dr, and so the first: with a = alpha * gate * w_post
+//   mean(a y dr) = mean(a y dR_out) + rstd_pre * (mean(a y d) - mean(d x) * mean(a y x)),
+// whose four sums are taken together, behind one barrier a row.
+//
 // Both are HBM streams: every input is read once and every output written once.
 // One workgroup holds a whole row in registers (eight values per thread and piece),
 // so the two means cost two workgroup reductions and no second pass over memory.
@@ -22,8 +26,8 @@
 //
 // Measured: forward 2048 x 8192 bf16 with both norms and a gate 22 us (134 MB, 6.1 TB/s);
 // one row of 8192 3.2 us; backward 4096 x 4096 float32 42 us (268 MB, 6.3 TB/s) and 4.3 for
-// the sums of the weights' gradients; 1777 x 5003 bf16 30 (107 MB, 3.5 TB/s: ten waves per
-// compute unit, whose two reductions a row the one row ahead does not cover) and 4.5.
+// the sums of the weights' gradients; 1777 x 5003 bf16 26 (107 MB, 4.1 TB/s: ten waves per
+// compute unit, and one row ahead does not cover a row's barrier; 30 with two) and 4.5.
 
 #include "norm.h"
 
@@ -170,6 +174,20 @@ QL_DEV float wg_sum(float v, float *red, int nw) {
 
 }  // namespace
 
+// The same for four sums behind one barrier.
+QL_DEV f32x4 wg_sum4(f32x4 v, f32x4 *red, int nw) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = wave_sum(v[i]);
+  if (nw == 1) return v;
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = red[0];
+#pragma unroll
+  for (int w = 1; w < kMaxWaves; ++w)
+    if (w < nw) v += red[w];
+  return v;
+}
+
 // Eight weights; ones where there are none (a product with 1 changes nothing).
 template <Rows K>
 QL_DEV Piece<float> weights(const float *w, const Cols<K> &q) {
@@ -286,7 +304,7 @@ __global__ __launch_bounds__(512) void norm_fwd_kernel(NormFwdArgs p, int shift)
 template <typename RT, int NV, bool SUMS, Rows K>
 __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs p, int shift, float *__restrict__ part) {
   constexpr bool AHEAD = NV == 1;
-  __shared__ float red[4][kMaxWaves];
+  __shared__ f32x4 red[4][kMaxWaves];
   const int tid = threadIdx.x, B = blockDim.x, nw = B >> 6;
   const int h = (int)p.h, skip = row_skip<K>(h, shift);
   const RT *Ro = reinterpret_cast<const RT *>(p.R_out), *dRo = reinterpret_cast<const RT *>(p.dR_out);
@@ -336,7 +354,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs p, int shift
   for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
     float d[NV][8], x[NV][8], y[NV][8], dr[NV][8];
     const float rp = rsp, rq = rsq;
-    float dot = 0.0f;
+    f32x4 sums4{0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const Cols<K> q(tid + B * j, skip, h);
@@ -347,18 +365,31 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs p, int shift
         y[j][i] = q.has(i) ? yy[j].get(i) * rq : 0.0f;
         d[j][i] = g * wp[j].get(i);
         dr[j][i] = q.has(i) ? dro[j].get(i) : 0.0f;
-        dot = __builtin_fmaf(d[j][i], x[j][i], dot);
+        sums4[0] = __builtin_fmaf(d[j][i], x[j][i], sums4[0]);
+        if (p.w_post) {  // the second mean's sum in the parts that the first one joins
+          const float ay = a[j][i] * y[j][i];
+          sums4[1] = __builtin_fmaf(ay, dr[j][i], sums4[1]);
+          sums4[2] = __builtin_fmaf(ay, d[j][i], sums4[2]);
+          sums4[3] = __builtin_fmaf(ay, x[j][i], sums4[3]);
+        }
         if constexpr (SUMS) sum(0, j, i) = __builtin_fmaf(g, x[j][i], sum(0, j, i));
       }
     }
     if (AHEAD) load(m + gridDim.x);
+    float mean = 0.0f, mean_post = 0.0f;
+    if (p.w_post) {
+      sums4 = wg_sum4(sums4, red[slot], nw) * inv_h;
+      mean = sums4[0];
+      mean_post = sums4[1] + rp * (sums4[2] - mean * sums4[3]);
+    } else if (p.w_pre) {
+      mean = wg_sum(sums4[0], reinterpret_cast<float *>(red[slot]), nw) * inv_h;
+    }
+    slot = (slot + 1) & 3;
     if (p.w_pre) {
-      dot = wg_sum(dot, red[slot], nw) * inv_h;
-      slot = (slot + 1) & 3;
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dr[j][i] += rp * (d[j][i] - x[j][i] * dot);
+        for (int i = 0; i < 8; ++i) dr[j][i] += rp * (d[j][i] - x[j][i] * mean);
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -366,7 +397,6 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs p, int shift
       store8(dR + m * h, dr[j], q);
     }
     if (p.dY) {
-      dot = 0.0f;
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
@@ -374,16 +404,8 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs p, int shift
           // without a norm after the block y is Y, and the gradient ends here
           if constexpr (SUMS) sum(1, j, i) = __builtin_fmaf(dr[j][i], y[j][i], sum(1, j, i));
           dr[j][i] *= a[j][i];
-          dot = __builtin_fmaf(dr[j][i], y[j][i], dot);
+          if (p.w_post) dr[j][i] = rq * (dr[j][i] - y[j][i] * mean_post);
         }
-      if (p.w_post) {
-        dot = wg_sum(dot, red[slot], nw) * inv_h;
-        slot = (slot + 1) & 3;
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) dr[j][i] = rq * (dr[j][i] - y[j][i] * dot);
-      }
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const Cols<K> q(tid + B * j, skip, h);
