@@ -135,7 +135,8 @@ constexpr int lmax(int a, int b) { return a > b ? a : b; }
 // carry no loss, so they come straight from H and no list is made.  (A token is a column
 // of the product: what the others' rows hold stays in their own statistics, which nobody
 // reads.)  16 x 4096 x 32000: 63 us in all, with a list and a copy of the rows first 69.
-template <int BV, int BT, int WV, int SA, int SB, int BK, bool GRAD, bool FEW>
+// ONCE: the head is read past the caches (launch_logit_stats_few).
+template <int BV, int BT, int WV, int SA, int SB, int BK, bool GRAD, bool FEW, bool ONCE>
 __global__ __launch_bounds__(kThreads) void head_logits_kernel(LogitParams p) {
   constexpr int WT = 4 / WV, TA = BV / WV / 32, TB = BT / WT / 32;
   constexpr int kRing = (SA * BV + SB * BT) * BK;  // elements
@@ -155,7 +156,7 @@ __global__ __launch_bounds__(kThreads) void head_logits_kernel(LogitParams p) {
   gemm_tile_of(blockIdx.x, p.tiles_v, tiles_t, 4, tv, tt);
   const int64_t v0 = (int64_t)tv * BV, t0 = (int64_t)tt * BT;
   const int wa = wv / WT * (BV / WV), wb = wv % WT * (BT / WT);  // the wave's first row and column
-  RowOperand<BV, BK> A;
+  RowOperand<BV, BK, ONCE> A;
   std::conditional_t<FEW, RowOperand<BT, BK>, BlockRows<BT, BK>> B;
   A.init(p.h, lane, wv, wa);
   B.init(FEW ? p.h : p.h * 64, lane, wv, wb);
@@ -310,8 +311,8 @@ hipError_t logits(LogitParams &p, int64_t max_tokens, hipStream_t st) {
   p.tiles_v = GRAD ? 2 * (int)cdiv(p.nvoc, 256) : (int)cdiv(p.nvoc, 128);
   if constexpr (GRAD)
     if (max_tokens <= kFewTokens)
-      return launch(head_logits_kernel<128, 32, 4, 4, 4, 64, true, false>, (unsigned)p.tiles_v, kThreads, st, p);
-  return launch(head_logits_kernel<128, 128, 2, 3, 2, 64, GRAD, false>, (unsigned)(p.tiles_v * cdiv(max_tokens, 128)),
+      return launch(head_logits_kernel<128, 32, 4, 4, 4, 64, true, false, false>, (unsigned)p.tiles_v, kThreads, st, p);
+  return launch(head_logits_kernel<128, 128, 2, 3, 2, 64, GRAD, false, false>, (unsigned)(p.tiles_v * cdiv(max_tokens, 128)),
                 kThreads, st, p);
 }
 }  // namespace
@@ -321,7 +322,12 @@ hipError_t launch_logit_stats(LogitParams &p, int64_t max_tokens, hipStream_t st
 }
 hipError_t launch_logit_stats_few(LogitParams &p, hipStream_t st) {
   p.tiles_v = (int)cdiv(p.nvoc, 128);
-  return launch(head_logits_kernel<128, 32, 4, 4, 4, 64, false, true>, (unsigned)p.tiles_v, kThreads, st, p);
+  // A head larger than the last-level cache is read past it, which frees the way to memory
+  // (4096 values: 64000 words 105 -> 99 us; 8192 x 128256 462 -> 393 us); a smaller one is
+  // partly there at the next call (4096 x 32000: 41 us, read past the cache 54).
+  if (p.nvoc * p.h * 2 > ((int64_t)1 << 28))
+    return launch(head_logits_kernel<128, 32, 4, 4, 4, 64, false, true, true>, (unsigned)p.tiles_v, kThreads, st, p);
+  return launch(head_logits_kernel<128, 32, 4, 4, 4, 64, false, true, false>, (unsigned)p.tiles_v, kThreads, st, p);
 }
 hipError_t launch_logit_grad(LogitParams &p, int64_t max_tokens, hipStream_t st) {
   return logits<true>(p, max_tokens, st);

@@ -49,10 +49,17 @@ QL_DEV f32x16 lmfma(u32x4 a, u32x4 b, f32x16 c) {
 // dH and dW products of 4096 tokens x 8192 x 32000 took 2.4 and 2.2 instead of 1.6 ms.  (m0 is a reserved
 // register that the compiler writes right before each use of its own; these kernels have
 // none.)
+// ONCE: nobody reads the bytes again (streamed past the caches' other contents).
+template <bool ONCE = false>
 QL_DEV void lload_lds(u32x4 rsrc, int at, int voff, int soff) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-               :
-               : "s"(at), "v"(voff), "s"(rsrc), "s"(soff));
+  if constexpr (ONCE)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds"
+                 :
+                 : "s"(at), "v"(voff), "s"(rsrc), "s"(soff));
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :
+                 : "s"(at), "v"(voff), "s"(rsrc), "s"(soff));
 }
 QL_DEV u32x4 ltr_pair(const uint16_t *lo, const uint16_t *hi) {
   typedef __attribute__((address_space(3))) ls16x4 lds_s16x4;
@@ -76,7 +83,7 @@ constexpr int kWaves = 4;
 // A tile's descriptor (lrsrc) runs from its first row to the operand's end.  Row r's 16-byte
 // chunks sit at chunk ^ f(r), so that the 16 lanes of a read phase (one chunk of 16
 // consecutive rows) cover the 64 banks once.
-template <int R, int BK>
+template <int R, int BK, bool ONCE = false>
 struct RowOperand {
   static constexpr int kElems = R * BK;
   static constexpr int CH = BK / 8;               // chunks per row
@@ -104,7 +111,7 @@ struct RowOperand {
   // copy c of stage kt into the slot at LDS address `at`
   QL_DEV void copy(const u32x4 &rsrc, int at, int wv, int kt_, int c) const {
     const int kt = __builtin_amdgcn_readfirstlane(kt_);
-    lload_lds(rsrc, at + block(wv, c) * 1024, voff[c & 1], kt * BK * 2 + (c & ~1) * step);
+    lload_lds<ONCE>(rsrc, at + block(wv, c) * 1024, voff[c & 1], kt * BK * 2 + (c & ~1) * step);
   }
   QL_DEV u32x4 read(const uint16_t *stage, int lane, int t, int kk) const {
     return *reinterpret_cast<const u32x4 *>(stage + frag + t * 32 * BK + (((2 * kk + (lane >> 5)) ^ swz) << 3));

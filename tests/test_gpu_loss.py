@@ -171,6 +171,12 @@ def test_pieces_of_the_vocabulary_for_few_tokens(M):
     compare(run(*t), *t)
 
 
+def test_few_tokens_of_a_head_past_the_cache():
+    """A head of more than 256 MB, which is read another way."""
+    t = [x.to(DEV) for x in problem(9, 1024, 140001, "some")]
+    compare(run(*t), *t)
+
+
 @pytest.mark.parametrize("bad", [float("inf"), float("nan")])
 @pytest.mark.parametrize("M", [20, 70, 300])
 def test_a_gradient_that_is_not_finite_stays_with_its_token(M, bad):
