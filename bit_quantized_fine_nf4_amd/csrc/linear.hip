@@ -392,8 +392,8 @@ constexpr int kGradTile = 128;  // values of i per workgroup
 constexpr int grad_lds(int NT) { return 2 * 64 * (kGradTile + 8) + 2 * 64 * (16 * NT + 8); }  // elements
 
 template <int NT>
-QL_DEV void grad_tile(uint16_t *lds, const GradProblem &pr, int64_t tile, int rq, float s, int64_t M, int64_t mchunk,
-                      int64_t prows, float *__restrict__ part) {
+QL_DEV void grad_tile(uint16_t *lds, const GradProblem &pr, int64_t tile, int split, int splits, int rq, float s,
+                      int64_t M, int64_t mchunk, int64_t prows, float *__restrict__ part) {
   constexpr int RP = NT * 16;
   constexpr int LP = kGradTile + 8;                   // P slab row stride (elements)
   constexpr int PCH = 64 * kGradTile / 8 / 256;       // 16-byte P chunks per thread per slab
@@ -406,7 +406,7 @@ QL_DEV void grad_tile(uint16_t *lds, const GradProblem &pr, int64_t tile, int rq
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int g = lane >> 4, c16 = lane & 15;
   const int64_t i0 = tile * kGradTile;
-  const int64_t ms = (int64_t)blockIdx.y * mchunk;
+  const int64_t ms = (int64_t)split * mchunk;
   const int64_t me = ms + mchunk < M ? ms + mchunk : M;
   const int nsteps = (int)((me - ms + 63) / 64);
   const int64_t ldp = pr.ldp, ldq = pr.ldq;
@@ -527,8 +527,8 @@ QL_DEV void grad_tile(uint16_t *lds, const GradProblem &pr, int64_t tile, int rq
   }
 
   // D layout: lane (q = 16t + c16, g) holds rows i = 4g + v of each 16-row tile
-  if (gridDim.y > 1) {
-    float *out = part + ((int64_t)blockIdx.y * prows + pr.prow) * RP;
+  if (splits > 1) {
+    float *out = part + ((int64_t)split * prows + pr.prow) * RP;
 #pragma unroll
     for (int a = 0; a < 2; ++a)
 #pragma unroll
@@ -557,7 +557,8 @@ __global__ __launch_bounds__(256) void lora_grad_kernel(GradProblem pa, GradProb
                                                         int64_t mchunk, int64_t prows, float *__restrict__ part) {
   __shared__ __attribute__((aligned(16))) uint16_t lds[grad_lds(NT)];
   const bool second = blockIdx.x >= pa.tiles;
-  grad_tile<NT>(lds, second ? pb : pa, second ? blockIdx.x - pa.tiles : blockIdx.x, rq, s, M, mchunk, prows, part);
+  grad_tile<NT>(lds, second ? pb : pa, second ? blockIdx.x - pa.tiles : blockIdx.x, blockIdx.y, gridDim.y, rq, s, M,
+                mchunk, prows, part);
 }
 
 // Sum of the adapter gradients' token splits, in split order, scaled by s.  A
@@ -942,9 +943,11 @@ __global__ __launch_bounds__(kP16Threads) void lora_gradp_kernel(GradProblem pa,
 // own on the same accumulators: one bf16 U alone would leave dL1, a float32 result, with
 // 2^-9 errors.  The product is bound by reading X, not by the matrix cores.
 // The launch's other workgroups are dL2's: neither fills the chip alone, and the two
-// share one reduce launch (2048 tokens, 4096 x 4096, r = 16: 10.5 + 4.9 us, apart 8.4 +
-// 5.0 and 8.9; 8192 x 22016, r = 64: 44.5 + 7.2 us, apart 19.6 + 4.9 and 22.6 + 5.7).
-// Token splits are made for 512 workgroups, two to a compute unit (for 256: 12.0, 51.8 us).
+// share one reduce launch (2048 tokens, 4096 x 4096, r = 16: 9.4 + 4.6 us, apart 8.4 +
+// 5.0 and 8.9; 8192 x 22016, r = 64: 38.7 + 7.0 us, apart 19.6 + 4.9 and 22.6 + 5.7).
+// dL1's, with the generator and three products, take longer and start first (among the
+// others: 10.5, 44.5 us).  Token splits are made for 512 workgroups, two to a compute unit
+// (for 256: 12.0, 51.8 us; for 1024 as for 512).
 // ---------------------------------------------------------------------------
 QL_DEV void split3(float x, float &hi, float &mid, float &lo) {
   hi = bf16_lo(pack_bf16x2(x, 0.0f));
@@ -955,8 +958,9 @@ QL_DEV void split3(float x, float &hi, float &mid, float &lo) {
 constexpr int drop_lds(int NT) { return 2 * 64 * (kGradTile + 8) + 3 * 64 * (16 * NT + 8); }  // elements
 
 template <int NT>
-QL_DEV void drop_tile(uint16_t *lds, const GradProblem &pr, const float *U, const DropState &drop, int rq, float s,
-                      int64_t M, int64_t mchunk, int64_t prows, float *__restrict__ part) {
+QL_DEV void drop_tile(uint16_t *lds, const GradProblem &pr, const float *U, const DropState &drop, int64_t tile,
+                      int split, int splits, int rq, float s, int64_t M, int64_t mchunk, int64_t prows,
+                      float *__restrict__ part) {
   constexpr int RP = NT * 16;
   constexpr int LP = kGradTile + 8, LQ = RP + 8;
   constexpr int PCH = 64 * kGradTile / 8 / 256;  // 16-byte pieces of X per thread and slab (4)
@@ -965,8 +969,8 @@ QL_DEV void drop_tile(uint16_t *lds, const GradProblem &pr, const float *U, cons
   uint16_t (*Qs)[64 * LQ] = reinterpret_cast<uint16_t (*)[64 * LQ]>(lds + 2 * 64 * LP);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int g = lane >> 4, c16 = lane & 15;
-  const int64_t i0 = (int64_t)blockIdx.x * kGradTile;
-  const int64_t ms = (int64_t)blockIdx.y * mchunk;
+  const int64_t i0 = tile * kGradTile;
+  const int64_t ms = (int64_t)split * mchunk;
   const int64_t me = ms + mchunk < M ? ms + mchunk : M;
   const int nsteps = (int)((me - ms + 63) / 64);
   const int64_t ldp = pr.ldp;
@@ -1047,7 +1051,7 @@ QL_DEV void drop_tile(uint16_t *lds, const GradProblem &pr, const float *U, cons
     __syncthreads();  // U's parts are overwritten next
   }
   // D layout: lane (q = 16t + c16, g) holds rows i = 4g + v of each 16-row tile
-  float *out = gridDim.y > 1 ? part + (int64_t)blockIdx.y * prows * RP : pr.out;
+  float *out = splits > 1 ? part + (int64_t)split * prows * RP : pr.out;
 #pragma unroll
   for (int a = 0; a < 2; ++a)
 #pragma unroll
@@ -1057,7 +1061,7 @@ QL_DEV void drop_tile(uint16_t *lds, const GradProblem &pr, const float *U, cons
         const int64_t i = i0 + wave * 32 + 16 * a + 4 * g + v;
         const int q = t * 16 + c16;
         if (i >= pr.I) continue;
-        if (gridDim.y > 1) out[i * RP + q] = acc[a][t][v];
+        if (splits > 1) out[i * RP + q] = acc[a][t][v];
         else if (q < rq) out[i * rq + q] = s * acc[a][t][v];
       }
 }
@@ -1181,11 +1185,15 @@ T *at(void *ws, size_t off) { return reinterpret_cast<T *>(reinterpret_cast<char
 
 template <int NT>
 __global__ __launch_bounds__(256) void drop_grad_kernel(GradProblem pa, GradProblem pb, const float *U, DropState drop,
-                                                        int rq, float s, int64_t M, int64_t mchunk, int64_t prows,
-                                                        float *__restrict__ part) {
+                                                        int splits, int rq, float s, int64_t M, int64_t mchunk,
+                                                        int64_t prows, float *__restrict__ part) {
   __shared__ __attribute__((aligned(16))) uint16_t lds[drop_lds(NT)];
-  if (blockIdx.x < pa.tiles) drop_tile<NT>(lds, pa, U, drop, rq, s, M, mchunk, prows, part);
-  else grad_tile<NT>(lds, pb, blockIdx.x - pa.tiles, rq, s, M, mchunk, prows, part);
+  // dL1's workgroups, which take longer, start first
+  const bool second = blockIdx.x >= pa.tiles * splits;
+  const int64_t id = second ? blockIdx.x - pa.tiles * splits : blockIdx.x, tiles = second ? pb.tiles : pa.tiles;
+  const int split = (int)(id / tiles);
+  if (!second) drop_tile<NT>(lds, pa, U, drop, id - split * tiles, split, splits, rq, s, M, mchunk, prows, part);
+  else grad_tile<NT>(lds, pb, id - split * tiles, split, splits, rq, s, M, mchunk, prows, part);
 }
 
 // DROP: dropout on the forward's X (kn)
@@ -1751,12 +1759,12 @@ DropLayout drop_layout(int64_t M, int64_t h, int64_t o, int r) {
 hipError_t drop_grad(const GradProblem &pa, const GradProblem &pb, const float *U, const DropState &d, int r, float s,
                      int64_t M, int RP16, const Split &sp, float *part, hipStream_t st) {
   const int64_t prows = pa.I + pb.I;
-  const dim3 grid((unsigned)(pa.tiles + pb.tiles), (unsigned)sp.S);
+  const unsigned grid = (unsigned)((pa.tiles + pb.tiles) * sp.S);
   hipError_t e = hipErrorInvalidValue;
   switch (RP16 / 16) {
 #define QL_DG(NT)                                                                                                \
   case NT:                                                                                                       \
-    e = launch(drop_grad_kernel<NT>, grid, 256, st, pa, pb, U, d, r, s, M, sp.chunk, prows, part);               \
+    e = launch(drop_grad_kernel<NT>, grid, 256, st, pa, pb, U, d, sp.S, r, s, M, sp.chunk, prows, part);         \
     if (e == hipSuccess && sp.S > 1)                                                                             \
       e = launch(lora_grad_reduce_kernel<NT * 16>, (unsigned)(prows / kGradRedRows), 256, st, pa, pb, r, s, sp.S, \
                  prows, (const float *)part);                                                                    \
