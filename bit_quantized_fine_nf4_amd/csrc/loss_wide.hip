@@ -182,6 +182,31 @@ QL_DEV u32x4 eight(const float (&a)[4], const float (&b)[4]) {
   return u32x4{x[0], y[0], x[1], y[1]};
 }
 
+// Stores in whole lines.  Lane l holds four pieces of row l % 32 of a wave's 32 x 32 (or 32 x
+// 64) outputs; piece k of both 32-lane halves is 32 bytes of the row's 128.  Afterwards v[j]
+// is row 8 row_group(j) + l % 8, and the piece is that of lane_piece(l): a store covers eight
+// lines instead of a quarter of 32.  Lanes 16 apart are swapped first, then lanes 8 apart.
+QL_DEV void by_lines(u32x4 (&v)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; k += 2)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const auto x = __builtin_amdgcn_permlane16_swap(v[k][e], v[k + 1][e], false, false);
+      v[k][e] = x[0];
+      v[k + 1][e] = x[1];
+    }
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int a = (int)v[k][e], b = (int)v[k + 2][e];
+      v[k][e] = (uint32_t)__builtin_amdgcn_update_dpp(a, b, 0x128, 0xF, 0xC, false);  // row_ror:8
+      v[k + 2][e] = (uint32_t)__builtin_amdgcn_update_dpp(b, a, 0x128, 0xF, 0x3, false);
+    }
+}
+QL_DEV constexpr int row_group(int j) { return (j >> 1) | (j & 1) << 1; }
+QL_DEV int lane_piece(int lane) { return ((lane >> 4) & 1) | ((lane >> 3) & 1) << 1; }
+
 }  // namespace
 
 // GRAD false: part[half of a tile][token] = (max, sum of exp(z - max)) over 128
@@ -354,18 +379,26 @@ __global__ __launch_bounds__(kThreads) void head_dh_wide_kernel(HeadGradParams p
       float *out = p.part + (int64_t)(u / tiles) * n * p.h;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int64_t t = (int64_t)tt * kT + wb + 32 * j + l32;
-        float *dst = out + t * p.h;
+        const int64_t t0 = (int64_t)tt * kT + wb + 32 * j + (lane & 7);
 #pragma unroll
-        for (int ii = 0; ii < 4; ++ii)
+        for (int ii = 0; ii < 4; ++ii) {
+          u32x4 w[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int64_t c = (int64_t)th * kT + wa + 32 * ii + 8 * q + 4 * g;
+          for (int q = 0; q < 4; ++q)
+            w[q] = __builtin_bit_cast(u32x4, f32x4{acc[ii][j][4 * q], acc[ii][j][4 * q + 1], acc[ii][j][4 * q + 2],
+                                                   acc[ii][j][4 * q + 3]});
+          by_lines(w);
+          const int64_t c = (int64_t)th * kT + wa + 32 * ii + 8 * lane_piece(lane) + 4 * g;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int64_t t = t0 + 8 * row_group(k);
             if (t >= n || c >= p.h) continue;
-            f32x4 v{acc[ii][j][4 * q], acc[ii][j][4 * q + 1], acc[ii][j][4 * q + 2], acc[ii][j][4 * q + 3]};
-            if (p.add) v += *reinterpret_cast<const f32x4 *>(dst + c);
-            *reinterpret_cast<f32x4 *>(dst + c) = v;
+            f32x4 v = __builtin_bit_cast(f32x4, w[k]);
+            float *dst = out + t * p.h + c;
+            if (p.add) v += *reinterpret_cast<const f32x4 *>(dst);
+            *reinterpret_cast<f32x4 *>(dst) = v;
           }
+        }
       }
     }
     u = unit_of(wg, i, units);
@@ -425,21 +458,27 @@ __global__ __launch_bounds__(kThreads) void head_dw_wide_kernel(HeadGradParams p
       tile_of(u, tiles_h, tiles_v, th, tv);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int64_t v = (int64_t)tv * kT + wb + 32 * j + l32;
-        uint16_t *dst = p.dW + v * p.h;
+        const int64_t v0 = (int64_t)tv * kT + wb + 32 * j + (lane & 7);
 #pragma unroll
-        for (int ii = 0; ii < 4; ++ii)
+        for (int half = 0; half < 2; ++half) {
+          u32x4 w[4];
 #pragma unroll
-          for (int pp = 0; pp < 2; ++pp) {
+          for (int k = 0; k < 4; ++k) {
             float o[2][4];
 #pragma unroll
             for (int q = 0; q < 2; ++q)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) o[q][e] = top * acc[ii][j][8 * pp + 4 * q + e];
-            const u32x4 w = eight(o[0], o[1]);
-            const int64_t c = (int64_t)th * kT + wa + 32 * ii + 16 * pp + 8 * g;
-            if (v < p.nvoc && c < p.h) *reinterpret_cast<u32x4 *>(dst + c) = w;
+              for (int e = 0; e < 4; ++e) o[q][e] = top * acc[2 * half + (k >> 1)][j][8 * (k & 1) + 4 * q + e];
+            w[k] = eight(o[0], o[1]);
           }
+          by_lines(w);
+          const int64_t c = (int64_t)th * kT + wa + 64 * half + 16 * lane_piece(lane) + 8 * g;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int64_t v = v0 + 8 * row_group(k);
+            if (v < p.nvoc && c < p.h) *reinterpret_cast<u32x4 *>(p.dW + v * p.h + c) = w[k];
+          }
+        }
       }
     }
     u = unit_of(wg, i, units);
