@@ -9,6 +9,8 @@ namespace ql {
 //  X [M][ldx] bf16, codes [N][K/2], qabsmax [N][K/64], scale2 per 256 block scales,
 //  sT [M][ldt] bf16 with s applied (r > 0), L2 [r][N] bf16, Y [M][ldy] bf16.
 //  K and N are multiples of 64, 1 <= M <= 16.
+//  exact: the weight is the format's, bf16(level * a_hat), as the many-token GEMMs take
+//  it; otherwise bf16(level), with a_hat on each block's float32 sum.
 struct GemvParams {
   const uint16_t *X;
   int64_t ldx;
@@ -25,6 +27,7 @@ struct GemvParams {
   uint16_t *Y;
   int64_t ldy;
   float level[16];
+  bool exact;
 };
 
 hipError_t launch_nf4_gemv(const GemvParams &p, hipStream_t st);

@@ -26,6 +26,9 @@
 // 2(w/4)+1 with 16x16x32 MFMAs, tokens being the MFMA rows.  The B operand is
 // bf16(level[c]) from a byte -> bf16-pair table; a_hat multiplies each block's
 // float32 partial.  The waves' partial sums meet in LDS at the end.
+// With EXACT (also for one token) the B operand is the format's own weight
+// bf16(level[c] * a_hat), as in the many-token GEMMs: the table holds pairs of
+// float32 levels, and each pair costs two products and a conversion more.
 
 #include "gemv.h"
 
@@ -216,6 +219,8 @@ constexpr int kGvThreads = 512;      // 8 waves: wave w takes block w%4, row gro
 // Lookup table: 32 copies of the 256-entry table interleaved so that lane l
 // only touches banks l%32 and l%32 + 32 (conflict-free 32-lane phases).
 constexpr int kGvLutWords = 256 * 32;
+// EXACT: 16 copies of 8-byte entries, the same words
+constexpr int kGvPairCopies = 16;
 
 struct GvStage {
   u32x4 c;     // codes: 16 bytes of the stage tile
@@ -231,9 +236,9 @@ constexpr int kGvOOB = (int)0x80000000u;  // offset past every buffer: the load 
 
 // MT: token-count class (1, 4 or 16); output token 4g + v exists only for
 // v < MT when MT < 4, so the block-scale FMAs for absent tokens are skipped.
-template <int MT>
+template <int MT, bool EXACT>
 __global__ __launch_bounds__(kGvThreads) void nf4_gemv_kernel(GemvParams p) {
-  __shared__ uint32_t lut[kGvLutWords];
+  __shared__ __attribute__((aligned(16))) uint32_t lut[kGvLutWords];
   // stage tiles: codes [2][64 rows][128 B], activations [2][16 tokens][512 B];
   // reused for the cross-wave sum after the K loop
   __shared__ __attribute__((aligned(16))) uint8_t tiles[2 * kGvRows * kGvCodeB + 2 * 16 * kGvXB];
@@ -245,8 +250,8 @@ __global__ __launch_bounds__(kGvThreads) void nf4_gemv_kernel(GemvParams p) {
   if (tid < 16) lv[tid] = p.level[tid];
   __syncthreads();
   for (int i = tid; i < kGvLutWords; i += kGvThreads) {
-    const int e = i >> 5;  // word i = 32 e + copy
-    lut[i] = pack_bf16x2(lv[e >> 4], lv[e & 15]);
+    const int e = i >> 5;  // word i = 32 e + copy; EXACT: 32 e + 2 copy + weight of the pair
+    lut[i] = !EXACT ? pack_bf16x2(lv[e >> 4], lv[e & 15]) : __builtin_bit_cast(uint32_t, lv[(i & 1) ? e & 15 : e >> 4]);
   }
 
   const int64_t n0 = (int64_t)blockIdx.x * kGvRows;
@@ -279,9 +284,12 @@ __global__ __launch_bounds__(kGvThreads) void nf4_gemv_kernel(GemvParams p) {
   auto load = [&](GvStage &R, int st) {
     R.c = __builtin_amdgcn_raw_buffer_load_b128(rc, voc, st * kGvCodeB, 0);
     R.x = __builtin_amdgcn_raw_buffer_load_b128(rx, st < xlim ? vox : kGvOOB, st * kGvXB, 0);
-    R.q = __builtin_amdgcn_raw_buffer_load_b8(rq, sthr ? voq : kGvOOB, 4 * st, 0);
+    // EXACT: blocks past the row's end take the mean for their scale, so that another row's
+    // infinite weight meets no zero activation
+    const bool on = sthr && (!EXACT || 4 * st + sblk < nblk);
+    R.q = __builtin_amdgcn_raw_buffer_load_b8(rq, on ? voq : kGvOOB, 4 * st, 0);
     R.s2 = __builtin_bit_cast(
-        float, __builtin_amdgcn_raw_buffer_load_b32(rs, sthr ? (int)(((sbase + 4 * st) >> 8) * 4) : kGvOOB, 0, 0));
+        float, __builtin_amdgcn_raw_buffer_load_b32(rs, on ? (int)(((sbase + 4 * st) >> 8) * 4) : kGvOOB, 0, 0));
   };
   auto store = [&](const GvStage &R, int buf) {
     *reinterpret_cast<u32x4 *>(&cbuf[buf][lc]) = R.c;
@@ -290,7 +298,7 @@ __global__ __launch_bounds__(kGvThreads) void nf4_gemv_kernel(GemvParams p) {
   };
   // compute role: token / feature index within a 16x16 MFMA tile, k-group
   const int n = lane & 15, g = lane >> 4;
-  const int lsel = lane & 31;
+  const int lsel = EXACT ? 2 * (lane % kGvPairCopies) : lane & 31;
   const int blk = wave & 3, rp = wave >> 2;
   const int pcw = 2 * blk + (g >> 1);  // code piece of this block for this k-group
   const int pxa = 8 * blk + 2 * g;     // activation pieces pxa, pxa + 1
@@ -303,10 +311,13 @@ __global__ __launch_bounds__(kGvThreads) void nf4_gemv_kernel(GemvParams p) {
   }
   constexpr int NV = MT < 4 ? MT : 4;
   float acc[2][NV];
+  f32x4 sum[2];  // EXACT
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+  for (int h = 0; h < 2; ++h) {
+    sum[h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int v = 0; v < NV; ++v) acc[h][v] = 0.0f;
+  }
   auto compute = [&](int buf) {
     const uint8_t *cb = cbuf[buf];
     const uint8_t *xb = xbuf[buf];
@@ -321,7 +332,19 @@ __global__ __launch_bounds__(kGvThreads) void nf4_gemv_kernel(GemvParams p) {
       for (int e = 0; e < 2; ++e) {
         const uint32_t w = e ? cw.y : cw.x;
 #pragma unroll
-        for (int t = 0; t < 4; ++t) bw[e][t] = lut[((w >> (8 * t)) & 0xFF) * 32 + lsel];
+        for (int t = 0; t < 4; ++t) {
+          const uint32_t *entry = lut + ((w >> (8 * t)) & 0xFF) * 32 + lsel;
+          if constexpr (EXACT) {
+            const f32x2 level = *reinterpret_cast<const f32x2 *>(entry);
+            bw[e][t] = pack_bf16x2(level[0] * ah[h], level[1] * ah[h]);
+          } else {
+            bw[e][t] = *entry;
+          }
+        }
+      }
+      if constexpr (EXACT) {
+        sum[h] = mfma16(a1, bw[1], mfma16(a0, bw[0], sum[h]));
+        continue;
       }
       f32x4 part = mfma16(a0, bw[0], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
       part = mfma16(a1, bw[1], part);
@@ -362,6 +385,11 @@ __global__ __launch_bounds__(kGvThreads) void nf4_gemv_kernel(GemvParams p) {
   // Cross-wave sum: acc[h][v] of wave (blk, rp) = partial Y[token 4g + v][row 16(2rp + h) + n]
   // red[block][token][row], rows padded to 68 floats: the 64 lanes of a store
   // (16 rows x 4 token groups) land in 64 distinct banks.
+  if constexpr (EXACT)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int v = 0; v < NV; ++v) acc[h][v] = sum[h][v];
   constexpr int kRedLd = 68;
   static_assert(4 * 16 * kRedLd * 4 <= sizeof(tiles), "reduction fits in the stage tiles");
   float *red = reinterpret_cast<float *>(tiles);
@@ -386,7 +414,7 @@ namespace {
 }  // namespace
 
 hipError_t launch_nf4_gemv(const GemvParams &p, hipStream_t st) {
-  if (p.M == 1 && p.K <= 16384) {
+  if (p.M == 1 && p.K <= 16384 && !p.exact) {
     const int64_t per = (p.N + kG1TargetWaves - 1) / kG1TargetWaves;
     const int rows = (int)(per < 1 ? 1 : per);
     const unsigned grid = (unsigned)((p.N + 4 * (int64_t)rows - 1) / (4 * (int64_t)rows));
@@ -394,7 +422,10 @@ hipError_t launch_nf4_gemv(const GemvParams &p, hipStream_t st) {
                        : launch(nf4_gemv1_kernel<8>, grid, kG1Threads, st, p, rows);
   }
   const unsigned grid = (unsigned)(p.N / kGvRows);
-  auto k = p.M == 1 ? nf4_gemv_kernel<1> : (p.M <= 4 ? nf4_gemv_kernel<4> : nf4_gemv_kernel<16>);
+  auto k = p.M == 1 ? nf4_gemv_kernel<1, false>
+                    : (p.M <= 4 ? nf4_gemv_kernel<4, false> : nf4_gemv_kernel<16, false>);
+  if (p.exact)
+    k = p.M == 1 ? nf4_gemv_kernel<1, true> : (p.M <= 4 ? nf4_gemv_kernel<4, true> : nf4_gemv_kernel<16, true>);
   return launch(k, grid, kGvThreads, st, p);
 }
 

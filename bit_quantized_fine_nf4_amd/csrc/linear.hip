@@ -1336,12 +1336,16 @@ int gemv_dx_chunks(int64_t h, int64_t o) {
 //     published in LDS by the 512 threads, one each.
 // The 4-bit read returns a byte's low nibble first, so lane i of a group holds
 // column i ^ 1 (the stored byte keeps the even column in its high nibble).
+// EXACT: the block scale rides on B instead.  The table holds pairs of float32 levels and
+// each entry becomes the format's weight, bf16(level * a_hat), as in the many-token GEMM;
+// A is dY as it is.
 // Columns past h decode whatever the buffer holds (finite levels) and are never
 // stored.  Chunks hold whole stages.
 constexpr int kGvmThreads = 512;             // 8 waves: one 64-column block each
 constexpr int kGvmRowB = kGvdCols / 2;       // code bytes of a stage row
 constexpr int kGvmBufs = 2;                  // code stages held in LDS (3, with 16 table copies: 5-10 % slower)
 constexpr int kGvmLutCopies = 32;            // interleaved copies of the byte table (fewer bank conflicts)
+constexpr int kGvmPairCopies = 16;           // EXACT: of 8-byte entries, the same space
 static_assert(kGvmThreads == kGvdCols && kGvmThreads == 8 * kGvmRows, "one wave per block, one a_hat per thread");
 static_assert(kGvmRows * kGvmRowB == 2 * 16 * kGvmThreads, "two 16-byte loads per thread and stage");
 
@@ -1361,15 +1365,18 @@ struct GvmRegs {
   float s2;      // its second-level scale
 };
 
+template <bool EXACT>
 __global__ __launch_bounds__(kGvmThreads) void nf4_gemv_dx_kernel(GvdParams p) {
   __shared__ __attribute__((aligned(16))) uint8_t cb[kGvmBufs][kGvmRows * kGvmRowB];
-  // lut[kGvmLutCopies * byte + copy] = bf16 pair (level[low nibble], level[high nibble])
-  __shared__ uint32_t lut[256 * kGvmLutCopies];
+  // lut[kGvmLutCopies * byte + copy] = bf16 pair (level[low nibble], level[high nibble]);
+  // EXACT: the two as float32, at [kGvmLutCopies * byte + 2 * copy]
+  __shared__ __attribute__((aligned(16))) uint32_t lut[256 * kGvmLutCopies];
   __shared__ __attribute__((aligned(16))) float ahs[2][kGvdCols / 64][kGvmRows];  // a_hat per [block][row]
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   for (int i = tid; i < 256 * kGvmLutCopies; i += kGvmThreads) {
     const int e = i / kGvmLutCopies;
-    lut[i] = pack_bf16x2(p.level[e & 15], p.level[e >> 4]);
+    lut[i] = !EXACT ? pack_bf16x2(p.level[e & 15], p.level[e >> 4])
+                    : __builtin_bit_cast(uint32_t, p.level[(i & 1) ? e >> 4 : e & 15]);
   }
   const int64_t h = p.h, nblk = h >> 6;
   const int64_t c0 = (int64_t)blockIdx.x * kGvdCols;
@@ -1399,7 +1406,7 @@ __global__ __launch_bounds__(kGvmThreads) void nf4_gemv_dx_kernel(GvdParams p) {
   // MFMA role: lane (i = lane % 16, g = lane / 16)
   const int i16 = lane & 15, g = lane >> 4;
   const int voy = (int)((i16 * p.ldy + n0 + 16 * g) * 2);  // tokens >= M: past the buffer, zero
-  const int lcopy = lane % kGvmLutCopies;
+  const int lcopy = EXACT ? 2 * (lane % kGvmPairCopies) : lane % kGvmLutCopies;
 
   auto load_codes = [&](int st_) {
     const int st = __builtin_amdgcn_readfirstlane(st_);
@@ -1436,14 +1443,17 @@ __global__ __launch_bounds__(kGvmThreads) void nf4_gemv_dx_kernel(GvdParams p) {
     const float *sp = &ahs[st & 1][wave][16 * g];
     const f32x4 s0 = *reinterpret_cast<const f32x4 *>(sp), s1 = *reinterpret_cast<const f32x4 *>(sp + 4);
     const f32x4 s2 = *reinterpret_cast<const f32x4 *>(sp + 8), s3 = *reinterpret_cast<const f32x4 *>(sp + 12);
-    const u32x4 A0{pack_bf16x2(bf16_lo(a0[0]) * s0[0], bf16_hi(a0[0]) * s0[1]),
-                   pack_bf16x2(bf16_lo(a0[1]) * s0[2], bf16_hi(a0[1]) * s0[3]),
-                   pack_bf16x2(bf16_lo(a0[2]) * s1[0], bf16_hi(a0[2]) * s1[1]),
-                   pack_bf16x2(bf16_lo(a0[3]) * s1[2], bf16_hi(a0[3]) * s1[3])};
-    const u32x4 A1{pack_bf16x2(bf16_lo(a1[0]) * s2[0], bf16_hi(a1[0]) * s2[1]),
-                   pack_bf16x2(bf16_lo(a1[1]) * s2[2], bf16_hi(a1[1]) * s2[3]),
-                   pack_bf16x2(bf16_lo(a1[2]) * s3[0], bf16_hi(a1[2]) * s3[1]),
-                   pack_bf16x2(bf16_lo(a1[3]) * s3[2], bf16_hi(a1[3]) * s3[3])};
+    u32x4 A0 = a0, A1 = a1;
+    if constexpr (!EXACT) {
+      A0 = u32x4{pack_bf16x2(bf16_lo(a0[0]) * s0[0], bf16_hi(a0[0]) * s0[1]),
+                 pack_bf16x2(bf16_lo(a0[1]) * s0[2], bf16_hi(a0[1]) * s0[3]),
+                 pack_bf16x2(bf16_lo(a0[2]) * s1[0], bf16_hi(a0[2]) * s1[1]),
+                 pack_bf16x2(bf16_lo(a0[3]) * s1[2], bf16_hi(a0[3]) * s1[3])};
+      A1 = u32x4{pack_bf16x2(bf16_lo(a1[0]) * s2[0], bf16_hi(a1[0]) * s2[1]),
+                 pack_bf16x2(bf16_lo(a1[1]) * s2[2], bf16_hi(a1[1]) * s2[3]),
+                 pack_bf16x2(bf16_lo(a1[2]) * s3[0], bf16_hi(a1[2]) * s3[1]),
+                 pack_bf16x2(bf16_lo(a1[3]) * s3[2], bf16_hi(a1[3]) * s3[3])};
+    }
     // lane i of group g names row 16 g + i; the block's bytes 32 w + 8 t .. + 7 are
     // logical chunk 2 w + t / 2, half t % 2
     const uint8_t *rowp = &cb[st % kGvmBufs][(16 * g + i16) * kGvmRowB];
@@ -1453,8 +1463,17 @@ __global__ __launch_bounds__(kGvmThreads) void nf4_gemv_dx_kernel(GvdParams p) {
       u32x4 b0, b1;
 #pragma unroll
       for (int d = 0; d < 4; ++d) {
-        b0[d] = lut[((v[0] >> (8 * d)) & 0xFF) * kGvmLutCopies + lcopy];
-        b1[d] = lut[((v[1] >> (8 * d)) & 0xFF) * kGvmLutCopies + lcopy];
+        const uint32_t *e0 = lut + ((v[0] >> (8 * d)) & 0xFF) * kGvmLutCopies + lcopy;
+        const uint32_t *e1 = lut + ((v[1] >> (8 * d)) & 0xFF) * kGvmLutCopies + lcopy;
+        if constexpr (EXACT) {  // rows 16 g + 2 d, + 1 and 16 g + 8 + 2 d, + 1
+          const f32x2 l0 = *reinterpret_cast<const f32x2 *>(e0), l1 = *reinterpret_cast<const f32x2 *>(e1);
+          const f32x4 r0 = d < 2 ? s0 : s1, r1 = d < 2 ? s2 : s3;
+          b0[d] = pack_bf16x2(l0[0] * r0[2 * d % 4], l0[1] * r0[2 * d % 4 + 1]);
+          b1[d] = pack_bf16x2(l1[0] * r1[2 * d % 4], l1[1] * r1[2 * d % 4 + 1]);
+        } else {
+          b0[d] = *e0;
+          b1[d] = *e1;
+        }
       }
       acc[t] = mfma16(A0, b0, acc[t]);
       acc[t] = mfma16(A1, b1, acc[t]);
@@ -1628,6 +1647,7 @@ hipError_t linear_fwd(const LinearArgs &a, const uint16_t *X, const uint16_t *L1
     gp.sT = sT; gp.ldt = L.RP64; gp.r = a.r; gp.L2 = L2;
     gp.Y = Y; gp.ldy = a.o;
     fill_levels(gp.level, tab);
+    gp.exact = drop && drop->threshold > 0;
     TimedLaunch tl(2, st);
     return launch_nf4_gemv(gp, st);
   }
@@ -1693,7 +1713,7 @@ hipError_t launch_linear_bwd(const LinearArgs &a, const uint16_t *X, const uint1
     }
     {
       TimedLaunch tl(1, st);
-      const hipError_t e = launch(nf4_gemv_dx_kernel, grid, kGvmThreads, st, vp);
+      const hipError_t e = launch(nf4_gemv_dx_kernel<false>, grid, kGvmThreads, st, vp);
       if (e != hipSuccess) return e;
     }
     const int64_t cg = (a.h / 8 + 63) / 64;
@@ -1726,6 +1746,9 @@ hipError_t launch_linear_bwd(const LinearArgs &a, const uint16_t *X, const uint1
 // T = (keep ⊙ X)·L1, Y = X·W_hat + s'·T·L2, dX = dY·W_hat^T + s'·keep ⊙ (U·L1^T),
 // dL1 = s'·(keep ⊙ X)^T·U, dL2 = s'·T^T·dY with s' = s / (1 - p): the scale is in s', so
 // that dropping an element is exact.
+// At most 16 tokens take the few-token kernels in their EXACT form, which multiply by the
+// format's weight as the GEMMs do; a call that drops nothing (threshold 0) is the plain
+// linear, whose few-token kernels take bf16(level) with the block scales apart.
 
 namespace {
 
@@ -1822,7 +1845,8 @@ hipError_t launch_linear_bwd_drop(const LinearArgs &a, const DropState &d, const
     vp.part = at<float>(ws, L.off_dxp);
     fill_levels(vp.level, tab);
     const dim3 grid((unsigned)((a.h + kGvdCols - 1) / kGvdCols), (unsigned)L.dxc);
-    e = launch(nf4_gemv_dx_kernel, grid, kGvmThreads, st, vp);
+    e = d.threshold > 0 ? launch(nf4_gemv_dx_kernel<true>, grid, kGvmThreads, st, vp)
+                        : launch(nf4_gemv_dx_kernel<false>, grid, kGvmThreads, st, vp);
     if (e != hipSuccess) return e;
     const int64_t cg = (a.h / 8 + 63) / 64;
     return launch(gemv_dx_finish_kernel, (unsigned)(a.M * cg), 256, st, (const float *)vp.part, L.dxc, (int)a.M,

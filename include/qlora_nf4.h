@@ -264,8 +264,11 @@ qlora_status_t qlora_linear_bwd_cb(const qlora_nf4_weight_t *W, qlora_codebook_t
  *   U = dY·L2^T                       dX = dY·W_hat^T + s'·keep ⊙ (U·L1^T)
  *   dL1 = s'·(keep ⊙ X)^T·U           dL2 = s'·T^T·dY
  *  T (bf16, without the scale) is the forward's output for the backward.  dL1 keeps U to
- *  float32's 24 bits.  The frozen part sees all of X.  Other arguments, layouts and errors
- *  as qlora_linear_fwd_cb and qlora_linear_bwd_cb; r = 0 is the plain linear.
+ *  float32's 24 bits.  The frozen part sees all of X.  W_hat is the bf16 dequantization at
+ *  every M.  Where nothing is dropped (t = 0) Y and dX are the plain linear's, which for
+ *  M <= 16 rounds the levels to bf16 and applies the block scales to sums (Y) or to dY in
+ *  bf16 (dX).  Other arguments, layouts and errors as qlora_linear_fwd_cb and
+ *  qlora_linear_bwd_cb; r = 0 is the plain linear.
  *  workspace: qlora_workspace_size(QLORA_OP_LINEAR_DROPOUT, M, h, o, r) bytes.
  */
 qlora_status_t qlora_dropout(const void *x, qlora_dtype_t dtype, int64_t n, double p, const uint64_t *rng, void *out,
