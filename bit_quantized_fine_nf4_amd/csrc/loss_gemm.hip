@@ -198,12 +198,13 @@ __global__ __launch_bounds__(kThreads) void head_logits_kernel(LogitParams p) {
     __syncthreads();
     if (threadIdx.x < BT) {
       const int64_t t = t0 + threadIdx.x;
-      f32x2 a = red[threadIdx.x];  // rows 0.. of the tile: never empty
+      f32x2 a = red[threadIdx.x];
 #pragma unroll
       for (int w = 1; w < WV; ++w) {
         const f32x2 b = red[w * BT + threadIdx.x];
         const float m = fmaxf(a[0], b[0]);
-        a = f32x2{m, a[1] * __expf(a[0] - m) + b[1] * __expf(b[0] - m)};
+        const float ref = m == -__builtin_inff() ? 0.0f : m;  // both waves' words masked: the sum is 0
+        a = f32x2{m, a[1] * __expf(a[0] - ref) + b[1] * __expf(b[0] - ref)};
       }
       if (t < n) p.part[(int64_t)tv * p.ldp + t] = a;
     }
