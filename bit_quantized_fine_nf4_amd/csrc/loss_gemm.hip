@@ -313,8 +313,20 @@ hipError_t logits(LogitParams &p, int64_t max_tokens, hipStream_t st) {
   if constexpr (GRAD)
     if (max_tokens <= kFewTokens)
       return launch(head_logits_kernel<128, 32, 4, 4, 4, 64, true, false, false>, (unsigned)p.tiles_v, kThreads, st, p);
-  return launch(head_logits_kernel<128, 128, 2, 3, 2, 64, GRAD, false, false>, (unsigned)(p.tiles_v * cdiv(max_tokens, 128)),
-                kThreads, st, p);
+  // A launch holds fewer than 2^32 threads.  Only statistics of h below 192 get there (131072
+  // tokens, 2^21 words: 2^24 workgroups): the vocabulary then takes several launches.
+  const int64_t tiles_t = cdiv(max_tokens, 128), most = (((int64_t)1 << 24) - 1) / tiles_t;
+  const int tiles_v = p.tiles_v;
+  for (int64_t first = 0; first < tiles_v; first += most) {
+    LogitParams q = p;
+    q.W += 128 * first * p.h, q.v0 += 128 * first, q.nvoc -= 128 * first;
+    if constexpr (!GRAD) q.part += first * p.ldp;
+    q.tiles_v = (int)(tiles_v - first < most ? tiles_v - first : most);
+    const hipError_t e = launch(head_logits_kernel<128, 128, 2, 3, 2, 64, GRAD, false, false>,
+                                (unsigned)(q.tiles_v * tiles_t), kThreads, st, q);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 }  // namespace
 
