@@ -37,6 +37,9 @@ bool valid_drop(double p, const uint64_t *rng, DropState &d) {
   d.threshold = (uint32_t)t;
   return true;
 }
+// M, h >= 1
+bool norm_supported(int64_t M, int64_t h) { return h <= kMaxNormWidth && M <= ((int64_t)1 << 40) / h; }
+
 double drop_scale(const DropState &d) { return 65536.0 / (65536.0 - d.threshold); }
 
 inline qlora_status_t launch_status(hipError_t e) { return e == hipSuccess ? QLORA_OK : QLORA_ERR_LAUNCH; }
@@ -224,7 +227,7 @@ qlora_status_t qlora_norm_fwd(const void *R, qlora_dtype_t r_dtype, const uint16
   if (!aligned16({R, Y, w_post, gate, w_pre, R_out, N, rstd_post, rstd_pre})) return QLORA_ERR_INVALID_VALUE;
   if (N && (N == R || N == Y || N == R_out)) return QLORA_ERR_INVALID_VALUE;
   if (R_out && R_out == Y) return QLORA_ERR_INVALID_VALUE;
-  if (h > kMaxNormWidth || M > ((int64_t)1 << 40) / h) return QLORA_ERR_UNSUPPORTED;
+  if (!norm_supported(M, h)) return QLORA_ERR_UNSUPPORTED;
   const NormFwdArgs a{R, Y, w_post, gate, w_pre, alpha, eps, M, h, Y ? R_out : nullptr, N,
                       w_post ? rstd_post : nullptr, rstd_pre};
   return launch_status(launch_norm_fwd(a, r_dtype == QLORA_BF16, reinterpret_cast<hipStream_t>(stream)));
@@ -245,7 +248,7 @@ qlora_status_t qlora_norm_bwd(const uint16_t *dN, const void *dR_out, qlora_dtyp
     return QLORA_ERR_INVALID_VALUE;
   if (dR == dN || dR == R_out || dR == Y || dR == dY) return QLORA_ERR_INVALID_VALUE;
   if (dY && (dY == dN || dY == R_out || dY == dR_out || dY == Y)) return QLORA_ERR_INVALID_VALUE;
-  if (h > kMaxNormWidth || M > ((int64_t)1 << 40) / h) return QLORA_ERR_UNSUPPORTED;
+  if (!norm_supported(M, h)) return QLORA_ERR_UNSUPPORTED;
   if (dw_pre || dw_post || dgate) {
     if (!workspace || !aligned(workspace, 256) || ws_bytes < round256(norm_bwd_workspace(M, h)))
       return QLORA_ERR_INVALID_VALUE;
@@ -319,12 +322,14 @@ qlora_status_t qlora_workspace_size(qlora_op_t op, int64_t a, int64_t b, int64_t
       *bytes = round256(linear_drop_workspace(a, b, c, r));
       return QLORA_OK;
     case QLORA_OP_NORM_BWD:
-      if (a < 1 || b < 1 || b > kMaxNormWidth) return QLORA_ERR_INVALID_VALUE;
+      if (a < 1 || b < 1) return QLORA_ERR_INVALID_VALUE;
+      if (!norm_supported(a, b)) return QLORA_ERR_UNSUPPORTED;
       *bytes = round256(norm_bwd_workspace(a, b));
       return QLORA_OK;
     case QLORA_OP_LOSS_FWD:
     case QLORA_OP_LOSS_BWD:
-      if (a < 1 || c < 1 || b < 64 || b % 64 || !loss_supported(a, b, c)) return QLORA_ERR_INVALID_VALUE;
+      if (a < 1 || c < 1 || b < 64 || b % 64) return QLORA_ERR_INVALID_VALUE;
+      if (!loss_supported(a, b, c)) return QLORA_ERR_UNSUPPORTED;
       *bytes = round256(op == QLORA_OP_LOSS_FWD ? loss_fwd_workspace(a, b, c) : loss_bwd_workspace(a, b, c));
       return QLORA_OK;
   }

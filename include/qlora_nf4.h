@@ -386,10 +386,10 @@ qlora_status_t qlora_grad_sum(const uint16_t *const *parts, int32_t k, int64_t n
  *   N     = R_out * rstd(R_out) * w_pre
  * Arithmetic is float32 and each output is rounded once; N is formed from the
  * float32 R_out, before it is rounded to a bf16 stream.  M rows, 1 <= h <= 16384
- * (any h; a wider row is QLORA_ERR_UNSUPPORTED).  Y, N, dN and dY are [M][h] bf16;
- * the stream (R, R_out, dR_out, dR) is [M][h] of r_dtype; weights, gate and their
- * gradients are [h] float32, rstd_post and rstd_pre [M] float32.  All pointers are
- * 16-byte aligned.  Squares of magnitudes above 1e18 overflow float32: rows that
+ * (any h; a wider row, or more than 2^40 values, is QLORA_ERR_UNSUPPORTED).  Y, N,
+ * dN and dY are [M][h] bf16; the stream (R, R_out, dR_out, dR) is [M][h] of r_dtype;
+ * weights, gate and their gradients are [h] float32, rstd_post and rstd_pre [M]
+ * float32.  All pointers are 16-byte aligned.  Squares of magnitudes above 1e18 overflow float32: rows that
  * hold such values give unspecified results, like non-finite ones.
  *
  * qlora_norm_fwd
@@ -456,7 +456,8 @@ qlora_status_t qlora_loss_bwd(const uint16_t *H, const uint16_t *W, const int64_
                               const float *dloss, int64_t M, int64_t h, int64_t V, uint16_t *dH, uint16_t *dW,
                               void *workspace, size_t ws_bytes, void *stream);
 
-/* Workspace bytes an entry point needs (always a multiple of 256; may be 0). */
+/* Workspace bytes an entry point needs (always a multiple of 256; may be 0).  Sizes past
+ * an entry point's limits give its QLORA_ERR_UNSUPPORTED here too. */
 qlora_status_t qlora_workspace_size(qlora_op_t op, int64_t a, int64_t b, int64_t c, int32_t r,
                                     size_t *bytes);
 
