@@ -364,8 +364,9 @@ LossLayout loss_layout(int64_t M, int64_t h, int64_t V, bool bwd) {
   L.top = take(4);
   L.idx = take((size_t)M * 4);
   L.label = take((size_t)M * 4);
-  const int64_t Mp = cdiv(M, 256) * 256;  // the blocked matrices' rows
-  L.hc = take((size_t)Mp * h * 2);
+  // The compact copy's rows: whole blocks (readers stop there); none where the forward takes
+  // H as it is.
+  L.hc = take(!bwd && M <= kFewTokens ? 0 : (size_t)(cdiv(M, 32) * 32) * h * 2);
   if (!bwd) {
     L.stat = take((size_t)logit_parts(M, h, V) * M * 8);
     L.zlab = take((size_t)M * 4);
@@ -373,7 +374,10 @@ LossLayout loss_layout(int64_t M, int64_t h, int64_t V, bool bwd) {
     L.lse = take((size_t)M * 4);
     L.dloss = take((size_t)M * 4);
     L.piece = loss_piece(M, V);
-    L.g = take((size_t)Mp * L.piece * 2);
+    // G's rows: whole tiles of the kernel that writes them (a row more than M costs 2 bytes a
+    // word: one token of 2^20 words takes 64 MB)
+    const int64_t tile = M <= kFewTokens ? kFewTokens : M <= 128 ? 128 : 256;
+    L.g = take((size_t)(cdiv(M, tile) * tile) * L.piece * 2);
     L.rows = partial_rows(M);
     if (M <= 64) {
       L.kper = cdiv(cdiv(L.piece, few_splits(h, L.piece)), 64) * 64;
