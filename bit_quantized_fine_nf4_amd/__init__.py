@@ -187,9 +187,23 @@ class NF4Weight:
         return NF4WeightT(self.codes.data_ptr(), self.qabsmax.data_ptr(), self.scale2.data_ptr(),
                           self.mean.data_ptr(), self.h, self.o)
 
+    def check(self, device):
+        """Refuses parts that the C call would misread, which does not know their sizes: of
+        another type, too short, not contiguous or not on `device`."""
+        n = self.h * self.o
+        at = device.index
+        for name, t, dtype, least in (("codes", self.codes, torch.uint8, n // 2),
+                                      ("qabsmax", self.qabsmax, torch.int8, n // BLOCK),
+                                      ("scale2", self.scale2, torch.float32, -(-n // (BLOCK * CHUNK))),
+                                      ("mean", self.mean, torch.float32, 1)):
+            if t.dtype is not dtype or t.numel() < least or not t.is_contiguous() or t.get_device() != at:
+                raise ValueError(f"the weight's {name} must be a contiguous {dtype} tensor of {least} values on "
+                                 f"{device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+
     def call(self, name: str, *args):
         """Call entry point `name` on this weight: the NF4 entry point, or its `_cb` variant
         with the codebook for other codebooks."""
+        self.check(self.codes.device)  # (host codes: None, which no tensor's index is)
         wt = self.as_ctypes()
         if self.codebook == QLORA_CB_NF4:
             return getattr(lib, name)(ctypes.byref(wt), *args)
@@ -621,6 +635,7 @@ def _drop_check(W: NF4Weight, X, T, dY, L1, L2, outs):
                                   ("L1", L1, bf, (W.h, r)), ("L2", L2, bf, (r, W.o)),
                                   ("codes", W.codes, torch.uint8, (W.h * W.o // 2,))) + outs(M, r):
         _want(name, t, dtype, shape, dev)
+    W.check(dev)
     return M, r, dev
 
 
