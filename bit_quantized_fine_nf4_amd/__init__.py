@@ -640,10 +640,12 @@ def _drop_check(W: NF4Weight, X, T, dY, L1, L2, outs):
 
 
 def _drop_workspace(given, dev, M, W, r):
-    if given is None and workspace_size(QLORA_OP_LINEAR_DROPOUT, M, W.h, W.o, r) == 0:
-        return None, 0
-    ws = _workspace(QLORA_OP_LINEAR_DROPOUT, given, dev, M, W.h, W.o, r)
-    return _at(ws), ws.numel()
+    """The workspace, which the caller holds until its call is enqueued, or None where none is needed."""
+    if given is None:
+        size = workspace_size(QLORA_OP_LINEAR_DROPOUT, M, W.h, W.o, r)
+        return torch.empty(size, dtype=torch.uint8, device=dev) if size else None
+    _want("workspace", given, torch.uint8, (given.numel(),), dev)
+    return given
 
 
 def qlora_linear_fwd_dropout(W: NF4Weight, X: torch.Tensor, L1: Optional[torch.Tensor], L2: Optional[torch.Tensor],
@@ -654,9 +656,9 @@ def qlora_linear_fwd_dropout(W: NF4Weight, X: torch.Tensor, L1: Optional[torch.T
     M, r, dev = _drop_check(W, X, T, None, L1, L2, lambda M, r: (("Y", Y, torch.bfloat16, (M, W.o)),))
     Y = torch.empty(M, W.o, dtype=torch.bfloat16, device=dev) if Y is None else Y
     T = torch.empty(M, r, dtype=torch.bfloat16, device=dev) if T is None and r else T
-    ws, wb = _drop_workspace(workspace, dev, M, W, r)
+    ws = _drop_workspace(workspace, dev, M, W, r)
     _call(dev, "qlora_linear_fwd_dropout", ctypes.byref(W.as_ctypes()), W.codebook, _at(X), M, _at(L1), _at(L2), r,
-          float(s), float(p), _rng_state(rng, dev), _at(Y), _at(T), ws, wb)
+          float(s), float(p), _rng_state(rng, dev), _at(Y), _at(T), _at(ws), 0 if ws is None else ws.numel())
     return Y, T
 
 
@@ -674,7 +676,8 @@ def qlora_linear_bwd_dropout(W: NF4Weight, X: torch.Tensor, T: Optional[torch.Te
     if r:
         dL1 = torch.empty(W.h, r, dtype=torch.float32, device=dev) if dL1 is None else dL1
         dL2 = torch.empty(r, W.o, dtype=torch.float32, device=dev) if dL2 is None else dL2
-    ws, wb = _drop_workspace(workspace, dev, M, W, r)
+    ws = _drop_workspace(workspace, dev, M, W, r)
     _call(dev, "qlora_linear_bwd_dropout", ctypes.byref(W.as_ctypes()), W.codebook, _at(X), _at(T), _at(dY), M,
-          _at(L1), _at(L2), r, float(s), float(p), _rng_state(rng, dev), _at(dX), _at(dL1), _at(dL2), ws, wb)
+          _at(L1), _at(L2), r, float(s), float(p), _rng_state(rng, dev), _at(dX), _at(dL1), _at(dL2),
+          _at(ws), 0 if ws is None else ws.numel())
     return dX, dL1, dL2
