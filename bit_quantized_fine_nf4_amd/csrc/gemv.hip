@@ -28,7 +28,8 @@
 // float32 partial.  The waves' partial sums meet in LDS at the end.
 // With EXACT (also for one token) the B operand is the format's own weight
 // bf16(level[c] * a_hat), as in the many-token GEMMs: the table holds pairs of
-// float32 levels, and each pair costs two products and a conversion more.
+// float32 levels, and each pair costs two products and a conversion more (calls of
+// 8192 x 28672, r 16: 16 tokens 54 us for 46, one token 51 for the one-token kernel's 36).
 
 #include "gemv.h"
 

@@ -1338,7 +1338,8 @@ int gemv_dx_chunks(int64_t h, int64_t o) {
 // column i ^ 1 (the stored byte keeps the even column in its high nibble).
 // EXACT: the block scale rides on B instead.  The table holds pairs of float32 levels and
 // each entry becomes the format's weight, bf16(level * a_hat), as in the many-token GEMM;
-// A is dY as it is.
+// A is dY as it is (backward calls of 8192 x 28672, r 16: 16 tokens 105 us for 101, one 118
+// for 112).
 // Columns past h decode whatever the buffer holds (finite levels) and are never
 // stored.  Chunks hold whole stages.
 constexpr int kGvmThreads = 512;             // 8 waves: one 64-column block each

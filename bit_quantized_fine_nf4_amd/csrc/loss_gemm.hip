@@ -19,7 +19,7 @@
 // next stage's first reads.
 // Rows past an operand's end read as zero (buffer bounds).
 // 16 tokens of 4096 values, 32000 words (262 MB): logits 41 us where the head is partly in
-// the last-level cache, 50 to 60 from memory, as long as a plain read of it plus the start
+// the last-level cache, 50 to 62 from memory, as long as a plain read of it plus the start
 // and the softmax (deeper rings: no faster); dH 60 us.
 
 #include "loss_tiles.h"
@@ -336,8 +336,11 @@ hipError_t launch_logit_stats(LogitParams &p, int64_t max_tokens, hipStream_t st
 hipError_t launch_logit_stats_few(LogitParams &p, hipStream_t st) {
   p.tiles_v = (int)cdiv(p.nvoc, 128);
   // A head larger than the last-level cache is read past it, which frees the way to memory
-  // (4096 values: 64000 words 105 -> 99 us; 8192 x 128256 462 -> 393 us); a smaller one is
-  // partly there at the next call (4096 x 32000: 41 us, read past the cache 54).
+  // (4096 values: 64000 words 105 -> 99 us; 8192 x 128256 462 -> 393 us).  A smaller one may
+  // still be there from the call before, and reading it past the cache then costs more than
+  // it gains where it is not.  Whole calls of 16 tokens, 4096 x 32000: the same head again 44
+  // us, past the cache 65; eleven heads in turn, each from memory, 67 and 62.  4096 x 16384:
+  // 25 and 36; 39 and 37.
   if (p.nvoc * p.h * 2 > ((int64_t)1 << 28))
     return launch(head_logits_kernel<128, 32, 4, 4, 4, 64, false, true, true>, (unsigned)p.tiles_v, kThreads, st, p);
   return launch(head_logits_kernel<128, 32, 4, 4, 4, 64, false, true, false>, (unsigned)p.tiles_v, kThreads, st, p);

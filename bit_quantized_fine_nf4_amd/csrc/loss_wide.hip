@@ -22,7 +22,7 @@
 // Bound by the matrix cores at the clock that their load leaves (about 1.8 GHz): busy 74, 75,
 // 76 and 72 % of the cycles in the logits, the gradient, dH and dW of 4096 x 8192 x 32000,
 // which take 1.65, 1.65, 1.65 and 1.72 ms (1.25 to 1.31 PFLOP/s); no LDS bank conflicts.
-// With 1536 tokens 0.68, 0.68 and (dH, four splits) 0.72 ms.
+// With 1536 tokens 0.68, 0.68 and (dH, four splits) 0.72 ms; on a slower box 0.73, 0.73, 0.75.
 //
 // The MFMA's rows are the index that runs along the output's memory (the vocabulary for z
 // and G, the hidden width for dH and dW): a lane then holds four consecutive outputs, and

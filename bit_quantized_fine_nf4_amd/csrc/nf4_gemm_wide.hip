@@ -495,7 +495,7 @@ QL_DEV u32x2 wtr4(const uint8_t *ptr) {
 
 // DROP: dropout on the adapter's input.  The rank-r steps then run first, and the mask
 // clears the dropped elements' accumulators before the main loop (2048 tokens, 8192 x
-// 22016, r = 64: 665 us, without dropout 647).
+// 22016, r = 64: 665 us where without dropout it took 647; 678 to 769 on a slower box).
 template <bool DROP>
 __global__ __launch_bounds__(kThreads) void nf4_gemm_wide_dx_kernel(GemmParams p) {
   constexpr int kTN = kXTN, kBN = kXBN, kLdc = kXLdc;

@@ -17,8 +17,9 @@
 // whose four sums are taken together, behind one barrier a row.
 //
 // Both are HBM streams: every input is read once and every output written once.
-// One workgroup holds a whole row in registers (eight values per thread and piece),
-// so the two means cost two workgroup reductions and no second pass over memory.
+// One workgroup holds a whole row in registers (eight values per thread and piece), so
+// the means cost no second pass over memory: two workgroup reductions forward, one
+// backward.
 // The arithmetic is float32; each output is rounded once.  N is formed from the
 // float32 r, not from the stored R_out: for a bf16 stream that saves N one rounding.
 // Rows need not be 16-byte aligned (any h): gfx950 takes 16-byte global accesses at
