@@ -437,7 +437,9 @@ qlora_status_t qlora_norm_bwd(const uint16_t *dN, const void *dR_out, qlora_dtyp
  * again in pieces of the vocabulary, each turned into bf16 G (one rounding, then
  * float32 sums) in the workspace.  A token whose label is outside [0, V), such as
  * -100, carries no loss: its loss and lse are 0, its dH row is 0, it adds nothing to
- * dW, costs no products (but where all tokens are one tile), and its H row may hold anything.  Sums run in a fixed order.
+ * dW, costs no products (but where all tokens are one tile), and its H row may hold
+ * anything.  Sums run in a fixed order.
+ *  A word whose logit is -inf (a masked one) has probability 0, whole tiles of them too.
  *  M, V >= 1, h a positive multiple of 64.  h > 2^20, M or V > 2^24, or more than
  *  2^24 tiles of 256 tokens x 128 words are QLORA_ERR_UNSUPPORTED.
  *  H, W, dH, dW 16-byte aligned; labels 8; loss, lse, dloss 4; workspace 256.
