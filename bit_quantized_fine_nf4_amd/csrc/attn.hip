@@ -107,13 +107,14 @@ __global__ __launch_bounds__(kThreads * KG, 2) void attn_fwd_kernel(AttnArgs a, 
     }
     // the weights' phase first: it is what the wave beside this one, in its products, leaves room for
     __builtin_amdgcn_s_setprio(1);
+    if constexpr (FORM == kCapped) tanh_all(z, in2);
     if constexpr (FORM != kPlain) {
       const float away = (float)(k0 + 4 * g - (int)row);
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int v = 0; v < 16; ++v) {
-          const float x = FORM == kCapped ? cap2 * tanh_of(z[t][v] * in2) : z[t][v] * c;
+          const float x = z[t][v] * (FORM == kCapped ? cap2 : c);
           z[t][v] = __builtin_fmaf(-slope2, __builtin_fabsf(away + (float)(32 * t + acc_row(v, 0))), x);
         }
     }

@@ -192,17 +192,14 @@ __global__ __launch_bounds__(kThreads * KG, 2) void attn_dq_kernel(AttnArgs a, A
         z[1] = lmfma(f[kk % (kAhead + 1)][1], df[kk], z[1]);
         __builtin_amdgcn_sched_barrier(0);
       }
+      if constexpr (FORM == kCapped) tanh_all(reinterpret_cast<f32x16(&)[1]>(z[0]), in2);
 #pragma unroll
       for (int v = 0; v < 16; ++v) {
         const int j = 32 * t + acc_row(v, 0);
         float p, slack = 1.0f;
         if constexpr (FORM != kPlain) {
-          float x = z[0][v] * c;
-          if constexpr (FORM == kCapped) {
-            const float th = tanh_of(z[0][v] * in2);
-            x = cap2 * th;
-            slack = 1.0f - th * th;
-          }
+          const float x = z[0][v] * (FORM == kCapped ? cap2 : c);
+          if constexpr (FORM == kCapped) slack = 1.0f - z[0][v] * z[0][v];
           p = __builtin_amdgcn_exp2f(__builtin_fmaf(-slope2, __builtin_fabsf(away + (float)j), x) - lse2);
         } else {
           p = __builtin_amdgcn_exp2f(__builtin_fmaf(z[0][v], c, -lse2));
@@ -459,6 +456,7 @@ __global__ __launch_bounds__(kThreads * KG, 2) void attn_dkv_kernel(AttnArgs a, 
     const f32x4 *stat = reinterpret_cast<const f32x4 *>(lds.stat[kg][slot]);
     const float slope2 = FORM != kPlain && a.slopes ? a.slopes[head] * kLog2e : 0.0f;
     const float away = (float)(key - (q0 + 4 * g));
+    if constexpr (FORM == kCapped) tanh_all(reinterpret_cast<f32x16(&)[1]>(z[0]), in2);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const f32x4 s0 = stat[4 * q + 2 * g], s1 = stat[4 * q + 2 * g + 1];
@@ -468,12 +466,8 @@ __global__ __launch_bounds__(kThreads * KG, 2) void attn_dkv_kernel(AttnArgs a, 
         const int v = 4 * q + e;
         float p, slack = 1.0f;
         if constexpr (FORM != kPlain) {
-          float y = z[0][v] * c;
-          if constexpr (FORM == kCapped) {
-            const float th = tanh_of(z[0][v] * in2);
-            y = cap2 * th;
-            slack = 1.0f - th * th;
-          }
+          const float y = z[0][v] * (FORM == kCapped ? cap2 : c);
+          if constexpr (FORM == kCapped) slack = 1.0f - z[0][v] * z[0][v];
           p = __builtin_amdgcn_exp2f(__builtin_fmaf(-slope2, __builtin_fabsf(away - (float)(8 * q + e)), y) - lse2[e]);
         } else {
           p = __builtin_amdgcn_exp2f(__builtin_fmaf(z[0][v], c, -lse2[e]));

@@ -212,9 +212,50 @@ QL_DEV float both_halves_sum(float x) {
   return __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
 }
 
-// tanh(x) from exp(2 x): 1 - 2 / (exp(2 x) + 1), right at both ends (exp's 0 and infinity).
-// x2 = 2 x log2(e).
-QL_DEV float tanh_of(float x2) { return 1.0f - 2.0f * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(x2) + 1.0f); }
+// tanh(t) of x = 2 t log2(e), to a few roundings of itself however small it is: a capped score
+// is the cap times it, so an error of the size of 1's rounding would grow with the cap.  From
+// |t| = 1/2 on 1 - 2 / (exp(2 t) + 1), right at both ends (exp's 0 and infinity); below, where
+// that cancels, x P(x^2) with P fitted to tanh(t) / x by least squares of the relative error at
+// Chebyshev's points, which leaves 2^-26.  Scores of a cap in use hardly ever pass half of it, so
+// a wave looks its values over first and takes the exponentials only if one does: step of 1531
+// tokens, 24 heads of 64, cap 30 109 us, by exponentials alone 123, by both everywhere 141; of 2048
+// tokens, 32 heads of 128, cap 30 253 (251), cap 4, which most tiles pass half of, 302 (251).
+constexpr float kTanhSmall = 1.4426950408889634f;  // |x| at |t| = 1/2
+template <bool FAR>
+QL_DEV float tanh_of(float x) {
+  const float s = x * x;
+  float p = __builtin_fmaf(1.23535186e-06f, s, -3.18191771e-05f);
+  p = __builtin_fmaf(p, s, 6.66246258e-04f);
+  p = __builtin_fmaf(p, s, -1.38759156e-02f);
+  p = x * __builtin_fmaf(p, s, 3.46573586e-01f);
+  if constexpr (!FAR) return p;
+  const float far = 1.0f - 2.0f * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(x) + 1.0f);
+  return __builtin_fabsf(x) < kTanhSmall ? p : far;
+}
+// scores -> tanh of each times `in`
+template <typename X, int N>
+QL_DEV void tanh_all(X (&z)[N], float in) {
+  constexpr int kEach = sizeof(X) / 4;
+  float most = 0.0f;
+#pragma unroll
+  for (int t = 0; t < N; ++t)
+#pragma unroll
+    for (int v = 0; v < kEach; ++v) {
+      z[t][v] *= in;
+      most = fmaxf(most, __builtin_fabsf(z[t][v]));
+    }
+  if (__any(most >= kTanhSmall)) {
+#pragma unroll
+    for (int t = 0; t < N; ++t)
+#pragma unroll
+      for (int v = 0; v < kEach; ++v) z[t][v] = tanh_of<true>(z[t][v]);
+  } else {
+#pragma unroll
+    for (int t = 0; t < N; ++t)
+#pragma unroll
+      for (int v = 0; v < kEach; ++v) z[t][v] = tanh_of<false>(z[t][v]);
+  }
+}
 
 // Span of a query, clamped to the tokens; an empty one is (INT_MAX, 0), which sees nothing
 // and leaves a union of spans as it is.

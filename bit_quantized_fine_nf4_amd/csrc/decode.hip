@@ -275,19 +275,15 @@ __global__ __launch_bounds__(kThreads) void decode_attn_kernel(DecodeArgs a, int
       }
       if (j0 < from) bits &= ~0u << (from - j0);
       if (end - j0 < kStep) bits &= (1u << (end - j0)) - 1;
+      if constexpr (FORM == kCapped) tanh_all(z, in2);
       float mx = -__builtin_inff();
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           const int at = 16 * t + 4 * g4 + v;
-          float x;
-          if constexpr (FORM != kPlain) {
-            x = FORM == kCapped ? cap2 * tanh_of(z[t][v] * in2) : z[t][v] * c;
-            x = __builtin_fmaf(-slope2, (float)(n - 1 - (j0 + at)), x);
-          } else {
-            x = z[t][v] * c;
-          }
+          float x = z[t][v] * (FORM == kCapped ? cap2 : c);
+          if constexpr (FORM != kPlain) x = __builtin_fmaf(-slope2, (float)(n - 1 - (j0 + at)), x);
           x = bits >> at & 1 ? x : -__builtin_inff();
           z[t][v] = x;
           mx = fmaxf(mx, x);
