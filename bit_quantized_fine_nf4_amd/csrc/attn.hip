@@ -226,7 +226,8 @@ __global__ __launch_bounds__(kThreads * KG, 2) void attn_fwd_kernel(AttnArgs a, 
     sum = __builtin_fmaf(to, other[1], by * sum);
     top = both;
   }
-  const bool any = span.lo < span.hi && sum > 0.0f;
+  // (a sum that is not a number is no row without keys: it goes on into O and lse)
+  const bool any = span.lo < span.hi && !(sum == 0.0f);
   store_row<D>(O + (row * a.hq + head) * a.d, acc, any ? 1.0f / sum : 0.0f, live, a.d, g);
   if (live && g == 0)
     lse[(int64_t)head * a.M + row] = any ? (top + __builtin_amdgcn_logf(sum)) * kLn2 : -__builtin_inff();
