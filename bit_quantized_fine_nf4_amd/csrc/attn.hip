@@ -84,11 +84,10 @@ __global__ __launch_bounds__(kThreads * KG, 2) void attn_fwd_kernel(AttnArgs a, 
     sv.copy(tv, k0, base + (2 + slot) * kTileBytes, wv);
   };
 
-  bool safe = false;
-  auto step = [&](int k0, int slot, bool masked) {
+  auto step = [&](int k0, int slot, bool masked, auto careful) {
+    constexpr bool kCareful = decltype(careful)::value;
     const uint32_t ks = base + slot * kTileBytes + read.row;
     const uint32_t vs = base + (2 + slot) * kTileBytes + read.col;
-    if (masked && safe) finite_tile<D, kKeys>(base + (2 + slot) * kTileBytes, lane);
     f32x16 z[2];
     zero(z);
     // fragments four groups ahead: all at once would not leave room for the sums
@@ -161,25 +160,40 @@ __global__ __launch_bounds__(kThreads * KG, 2) void attn_fwd_kernel(AttnArgs a, 
       p[2 * t + 1] = pack8(z[t], 1);
     }
     __builtin_amdgcn_s_setprio(0);
-    u32x4 vf[2][D / 32];
+    if constexpr (kCareful) {
 #pragma unroll
-    for (int t = 0; t < D / 32; ++t) vf[0][t] = col_frag<D>(vs, t, 0);
+      for (int b = 0; b < 4; ++b)
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      if (b < 3)
+        for (int t = 0; t < D / 32; ++t) {
+          u32x4 v = col_frag<D>(vs, t, b);
+          if (masked) v = finite(v);
+          acc[t] = lmfma(v, p[b], acc[t]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      if (masked) {
+        const uint32_t tile = base + (2 + slot) * kTileBytes;
+        for (uint64_t odd = odd_rows<D, kKeys>(tile, lane); odd; odd &= odd - 1) {
+          const int r = (int)__builtin_ctzll(odd);
+          spoil<D>(acc, tile, r, k0 + r >= span.lo && k0 + r < span.hi, g);
+        }
+      }
+    } else {
+      u32x4 vf[2][D / 32];
 #pragma unroll
-        for (int t = 0; t < D / 32; ++t) vf[b + 1 & 1][t] = col_frag<D>(vs, t, b + 1);
+      for (int t = 0; t < D / 32; ++t) vf[0][t] = col_frag<D>(vs, t, 0);
 #pragma unroll
-      for (int t = 0; t < D / 32; ++t) acc[t] = lmfma(vf[b & 1][t], p[b], acc[t]);
-      __builtin_amdgcn_sched_barrier(0);
+      for (int b = 0; b < 4; ++b) {
+        if (b < 3)
+#pragma unroll
+          for (int t = 0; t < D / 32; ++t) vf[b + 1 & 1][t] = col_frag<D>(vs, t, b + 1);
+#pragma unroll
+        for (int t = 0; t < D / 32; ++t) acc[t] = lmfma(vf[b & 1][t], p[b], acc[t]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
   };
 
-  // What masked tokens hold must not enter, but a weight of zero times an infinity or a NaN
-  // is NaN.  A pass that leaves a sum that is not finite is taken again with such values out
-  // of the way: to look for them in every masked tile took a third of such a tile's time.
-  // (A query that sees nothing may hold anything, in its own lanes.)
-  for (;;) {
+  auto walk = [&](auto careful) {
     zero(acc);
     top = -__builtin_inff(), sum = 0.0f;
     int slot = 0;
@@ -189,19 +203,22 @@ __global__ __launch_bounds__(kThreads * KG, 2) void attn_fwd_kernel(AttnArgs a, 
       tile_sync();
       if (k0 + KG * kKeys < last) fetch(k0 + KG * kKeys, slot ^ 1);
       if (k0 >= reach.hi || k0 + kKeys <= reach.lo) continue;  // nothing of this wave's
-      step(k0, slot, k0 < reach.all_lo || k0 + kKeys > reach.all_hi);
+      step(k0, slot, k0 < reach.all_lo || k0 + kKeys > reach.all_hi, careful);
     }
-    if (any_wave(span.lo < span.hi && !all_finite(acc), spoiled, wave, kWaves * KG) && !safe) {
-      safe = true;
-      continue;
-    }
-    break;
-  }
+  };
+  // What masked tokens hold must not enter, but a weight of zero times an infinity or a NaN
+  // is NaN.  A pass that leaves a sum that is not finite is taken again with zeros in the place
+  // of such values in masked tiles, and NaN for the queries that see them: to look for them in
+  // every masked tile took a third of such a tile's time.  (A query that sees nothing may hold
+  // anything, in its own lanes.)
+  walk(std::false_type{});
+  if (any_wave(span.lo < span.hi && !all_finite(acc), spoiled, wave, kWaves * KG)) walk(std::true_type{});
 
   sum = both_halves_sum(sum);
   if constexpr (KG > 1) {
     static_assert(KG == 2, "one group's results go to the other");
     f32x4 *join = reinterpret_cast<f32x4 *>(ring) + wv * (D / 8 * 64) + lane;
+    __syncthreads();  // the last tiles are read
     if (kg == 1) {
 #pragma unroll
       for (int t = 0; t < D / 32; ++t)

@@ -163,6 +163,48 @@ QL_DEV void finite_tile(uint32_t tile, int lane) {
   }
 }
 
+// What is not finite in a tile, for a pass that has to tell what a query sees from what it does
+// not.  A fragment with zeros in such places:
+QL_DEV u32x4 finite(u32x4 x) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t lo = (x[k] & 0x7F80u) == 0x7F80u ? 0u : 0xFFFFu;
+    const uint32_t hi = (x[k] & 0x7F800000u) == 0x7F800000u ? 0u : 0xFFFF0000u;
+    x[k] &= lo | hi;
+  }
+  return x;
+}
+// The rows of a tile (a bit each) that hold an infinity or a NaN:
+template <int D, int R>
+QL_DEV uint64_t odd_rows(uint32_t tile, int lane) {
+  bool odd = false;
+#pragma unroll 1
+  for (int c = 0; c < D / 8; ++c) {
+    const u32x4 x = *(LdsChunk *)(tile + lane % R * D * 2 + 16 * c);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) odd = odd || (x[k] & 0x7F80u) == 0x7F80u || (x[k] & 0x7F800000u) == 0x7F800000u;
+  }
+  const uint64_t rows = __ballot(odd);
+  return R == 64 ? rows : rows & ((1ull << (R & 63)) - 1);
+}
+// NaN into the sums of a lane that sees row r, where that row is not finite.
+template <int D>
+QL_DEV void spoil(f32x16 (&acc)[D / 32], uint32_t tile, int r, bool sees, int g) {
+  typedef __attribute__((address_space(3))) const u32x2 LdsPair;
+#pragma unroll
+  for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const u32x2 x = *(LdsPair *)(tile + r * D * 2 + (((4 * t + q) ^ fold<D>(r)) << 4) + 8 * g);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float v = i & 1 ? bf16_hi(x[i >> 1]) : bf16_lo(x[i >> 1]);
+        acc[t][4 * q + i] = __builtin_fmaf(sees ? v : 0.0f, 0.0f, acc[t][4 * q + i]);
+      }
+      __builtin_amdgcn_sched_barrier(0);  // (a few registers at a time)
+    }
+}
+
 // Whether every value of the accumulators is finite.
 template <int N>
 QL_DEV bool all_finite(const f32x16 (&x)[N]) {

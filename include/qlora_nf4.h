@@ -510,7 +510,8 @@ qlora_status_t qlora_rope(const uint16_t *Q, int64_t ldq, int32_t hq, const uint
  * A query that sees nothing has O = 0, lse = -inf, passes no gradient, and its rows of Q,
  * O, lse and dO may hold anything.  What a query does not see does not enter its results,
  * infinities and NaN included.  A NaN that a query holds or sees in a key makes its row of O
- * and its lse NaN.
+ * and its lse NaN; an infinity or NaN that it sees in a value leaves that column of its row of
+ * O not finite.
  * Query head h reads key head h / (hq / hk).
  *  Q [M][hq][d], K and V [M][hk][d] bf16 with token strides ldq, ldk, ldv; O, dO and the
  *  gradients are dense.  lse [hq][M] float32.  spans M x 2 int32, slopes hq float32 or NULL.

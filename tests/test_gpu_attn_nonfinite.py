@@ -104,6 +104,13 @@ def test_rows_of_a_nan(M, hq, hk, d, cap, kind, what):
     spoiled(M, hq, hk, d, cap, kind, what, NAN, ("O", "lse"))
 
 
+@pytest.mark.parametrize("value", [NAN, INF, -INF])
+@pytest.mark.parametrize("kind", ["causal", "documents"])
+@pytest.mark.parametrize("M,hq,hk,d,cap", SHAPES)
+def test_columns_of_a_value(M, hq, hk, d, cap, kind, value):
+    spoiled(M, hq, hk, d, cap, kind, "V", value, ("O", "lse"))
+
+
 def test_one_new_token():
     """The same of one new token: a NaN of a query or a seen key reaches its whole row, of a
     value its value."""
