@@ -39,6 +39,8 @@ constexpr int kRowsWg = 128;  // queries per workgroup
 constexpr int kKeysWg = 128;  // keys per workgroup
 constexpr int kTile = 64;     // keys per tile of attn_dq
 constexpr int kRows = 32;     // queries per tile of attn_dkv
+// attn_dq's passes: D by its own sum; dQ; dQ where what is not finite is looked for
+enum { kOwnD, kSums, kCarefulSums };
 constexpr int kFewKeys = 256;
 constexpr float kSteep = 1.0f / 16;  // of a bias
 
@@ -129,8 +131,9 @@ __global__ __launch_bounds__(kThreads * KG, 2) void attn_dq_kernel(AttnArgs a, A
     if (live) lse2 = gr.lse[(int64_t)head * a.M + row] * kLog2e;
     // rows that see nothing (and those past the last) carry no gradient
     if (!any) delta = 0.0f, lse2 = __builtin_inff();
-    // where rows are summed over, one that sees nothing has to be masked: no key is seen by all
-    const bool gap = __any(live && !any);
+    // where rows are summed over, one that sees nothing, or is past the last, has to be masked: no
+    // key is seen by all
+    const bool gap = __any(!any);
     if (head == 0 && kg == 0 && lane == 0)
       w.reach[row >> 5] = int4{reach.lo, reach.hi, gap ? 0x7FFFFFFF : reach.all_lo, reach.all_hi};
   }
@@ -165,11 +168,9 @@ __global__ __launch_bounds__(kThreads * KG, 2) void attn_dq_kernel(AttnArgs a, A
     sv.copy(tv, k0, base + (2 + slot) * kTileBytes, wv);
   };
   float own = 0.0f;  // D by its sum, of this lane half's keys
-  bool safe = false;
-  auto step = [&](int k0, int slot, bool masked, auto summing) {
-    constexpr bool kSum = decltype(summing)::value;
+  auto step = [&](int k0, int slot, bool masked, auto pass) {
+    constexpr bool kSum = decltype(pass)::value == kOwnD, kCareful = decltype(pass)::value == kCarefulSums;
     const uint32_t kt = base + slot * kTileBytes, vt = kt + 2 * kTileBytes;
-    if (!kSum && masked && safe) finite_tile<D, kTile>(kt, lane);
     const uint32_t kr = kt + read.row, vr = vt + read.row, kc = kt + read.col;
     const int from = span.lo - k0 - 4 * g, width = span.hi - span.lo;
     const float away = (float)(k0 + 4 * g - (int)row);
@@ -220,6 +221,16 @@ __global__ __launch_bounds__(kThreads * KG, 2) void attn_dq_kernel(AttnArgs a, A
       }
       const u32x4 ds[2] = {pack8(z[1], 0), pack8(z[1], 1)};
       constexpr int kTiles = D / 32, kColsAhead = 3;
+      if constexpr (kCareful) {
+#pragma unroll
+        for (int i = 0; i < 2 * kTiles; ++i) {
+          u32x4 k = col_frag<D>(kc, i % kTiles, 2 * t + i / kTiles);
+          if (masked) k = finite(k);
+          acc[i % kTiles] = lmfma(k, ds[i / kTiles], acc[i % kTiles]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        continue;
+      }
       u32x4 w[kColsAhead + 1];
 #pragma unroll
       for (int n = 0; n < kColsAhead; ++n) w[n] = col_frag<D>(kc, n % kTiles, 2 * t + n / kTiles);
@@ -231,8 +242,14 @@ __global__ __launch_bounds__(kThreads * KG, 2) void attn_dq_kernel(AttnArgs a, A
         __builtin_amdgcn_sched_barrier(0);
       }
     }
+    if constexpr (kCareful)
+      if (masked)
+        for (uint64_t odd = odd_rows<D, kTile>(kt, lane); odd; odd &= odd - 1) {
+          const int r = (int)__builtin_ctzll(odd);
+          spoil<D>(acc, kt, r, k0 + r >= span.lo && k0 + r < span.hi, g);
+        }
   };
-  auto walk = [&](auto summing) {
+  auto walk = [&](auto pass) {
     int slot = 0;
     if (first + kg * kTile < last) fetch(first + kg * kTile, 0);
     for (int at = first; at < last; at += KG * kTile, slot ^= 1) {
@@ -240,11 +257,11 @@ __global__ __launch_bounds__(kThreads * KG, 2) void attn_dq_kernel(AttnArgs a, A
       tile_sync();
       if (k0 + KG * kTile < last) fetch(k0 + KG * kTile, slot ^ 1);
       if (k0 >= reach.hi || k0 + kTile <= reach.lo) continue;
-      step(k0, slot, k0 < reach.all_lo || k0 + kTile > reach.all_hi, summing);
+      step(k0, slot, k0 < reach.all_lo || k0 + kTile > reach.all_hi, pass);
     }
   };
   if (few || (FORM != kPlain && slope2 >= kSteep * kLog2e)) {
-    walk(std::true_type{});
+    walk(std::integral_constant<int, kOwnD>{});
     own = both_halves_sum(own);
     if constexpr (KG > 1) {
       owns[kg][wv][lane] = own;
@@ -255,16 +272,17 @@ __global__ __launch_bounds__(kThreads * KG, 2) void attn_dq_kernel(AttnArgs a, A
     tile_sync();  // the last tile is read
   }
   if (kg == 0 && g == 0) w.stat[head * w.ld + row] = f32x2{lse2, delta};
+  zero(acc);
+  walk(std::integral_constant<int, kSums>{});
   // (as in the forward: taken again if what masked keys hold has spoiled a sum)
-  for (;;) {
+  if (any_wave(any && !all_finite(acc), spoiled, wave, kWaves * KG)) {
     zero(acc);
-    walk(std::false_type{});
-    if (!any_wave(any && !all_finite(acc), spoiled, wave, kWaves * KG) || safe) break;
-    safe = true;
+    walk(std::integral_constant<int, kCarefulSums>{});
   }
   if constexpr (KG > 1) {
     static_assert(KG == 2, "one group's sums go to the other");
     f32x4 *join = reinterpret_cast<f32x4 *>(ring) + wv * (D / 8 * 64) + lane;
+    __syncthreads();  // the last tiles are read
     if (kg == 1) {
 #pragma unroll
       for (int t = 0; t < D / 32; ++t)
@@ -419,15 +437,11 @@ __global__ __launch_bounds__(kThreads * KG, 2) void attn_dkv_kernel(AttnArgs a, 
     if (KG == 1 || kg == 1) s.copy(tv, k0 + 64, vt + 64 * D * 2, wv);
   }
   f32x16 dk[D / 32], dv[D / 32];
-  bool safe = false;
 
-  auto step = [&](int head, int q0, int slot, bool masked) {
+  auto step = [&](int head, int q0, int slot, bool masked, auto careful) {
+    constexpr bool kCareful = decltype(careful)::value;
     constexpr int kGroups = D / 16, kTiles = D / 32;
     const uint32_t qt = qt0 + slot * kTileBytes, ot = ot0 + slot * kTileBytes;
-    if (masked && safe) {
-      finite_tile<D, kRows>(qt, lane);
-      finite_tile<D, kRows>(ot, lane);
-    }
     const uint32_t qr = qt + read.row, dr = ot + read.row, vr = vt + 32 * wv * D * 2 + read.row;
     f32x16 z[2];  // scores, then p; dP, then dS
     zero(z);
@@ -497,6 +511,29 @@ __global__ __launch_bounds__(kThreads * KG, 2) void attn_dkv_kernel(AttnArgs a, 
 #pragma unroll
     for (int b = 0; b < 2; ++b) p[b][0] = pack8(z[0], b), p[b][1] = pack8(z[1], b);
     constexpr int kOps = 2 * kTiles, kAhead = 2;
+    if constexpr (kCareful) {
+#pragma unroll
+      for (int i = 0; i < kOps; ++i) {
+        const int b = i / kTiles, e = i % kTiles;
+        u32x4 o = col_frag<D>(oc, e, b), q = col_frag<D>(qc, e, b);
+        if (masked) o = finite(o), q = finite(q);
+        dv[e] = lmfma(o, p[b][0], dv[e]);
+        dk[e] = lmfma(q, p[b][1], dk[e]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (masked) {
+        const int *span = lds.span[kg][slot];
+        for (uint64_t odd = odd_rows<D, kRows>(ot, lane); odd; odd &= odd - 1) {
+          const int r = (int)__builtin_ctzll(odd);
+          spoil<D>(dv, ot, r, key >= span[2 * r] && key < span[2 * r + 1], g);
+        }
+        for (uint64_t odd = odd_rows<D, kRows>(qt, lane); odd; odd &= odd - 1) {
+          const int r = (int)__builtin_ctzll(odd);
+          spoil<D>(dk, qt, r, key >= span[2 * r] && key < span[2 * r + 1], g);
+        }
+      }
+      return;
+    }
     u32x4 w[kAhead + 1][2];
     auto cols = [&](int n) {
       w[n % (kAhead + 1)][0] = col_frag<D>(oc, n % kTiles, n / kTiles);
@@ -515,8 +552,7 @@ __global__ __launch_bounds__(kThreads * KG, 2) void attn_dkv_kernel(AttnArgs a, 
   };
 
   const int past = (hk + 1) * group;
-  // (as in the forward: taken again if what masked queries hold has spoiled a sum)
-  for (;;) {
+  auto walk = [&](auto careful) {
     zero(dk);
     zero(dv);
     int head = hk * group + hfirst, slot = 0;
@@ -530,12 +566,14 @@ __global__ __launch_bounds__(kThreads * KG, 2) void attn_dkv_kernel(AttnArgs a, 
       if (!hits && (head += hstep) < past) scan(0);  // the next head of the group
       tile_sync();
       if (hits) fetch(head, block + (int)__builtin_ctzll(hits) + kg, slot ^ 1);
-      if (seen) step(h, q0, slot, masked);
+      if (seen) step(h, q0, slot, masked, careful);
       slot ^= 1;
     }
-    if (!any_wave(!(all_finite(dk) && all_finite(dv)), lds.spoiled, wave, kWaves * KG) || safe) break;
-    safe = true;
-  }
+  };
+  walk(std::false_type{});
+  // (as in the forward: taken again if what masked queries hold has spoiled a sum)
+  if (any_wave(!(all_finite(dk) && all_finite(dv)), lds.spoiled, wave, kWaves * KG)) walk(std::true_type{});
+  __syncthreads();  // the last tiles are read
   __builtin_amdgcn_s_waitcnt(0);  // no copy may land after the workgroup's end
   if constexpr (KG > 1) {
     static_assert(KG == 2, "one group's sums go to the other");

@@ -128,41 +128,6 @@ QL_DEV u32x4 col_frag(uint32_t at, int t, int b) {
   return u32x4{ux[0], ux[1], uy[0], uy[1]};
 }
 
-// Infinities and NaN of a tile to zero.  A wave looks the tile over before it reads it; only
-// a tile that holds such a value is written to (a wave that sees that token's pair would
-// have had an unspecified result).
-template <int D, int R>
-QL_DEV void finite_tile(uint32_t tile, int lane) {
-  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
-  u16x2 most{0, 0};
-#pragma unroll
-  for (int i = 0; i < R * D / 512; ++i) {
-    const u32x4 x = *(LdsChunk *)(tile + 1024 * i + 16 * lane);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t m = x[k] & 0x7FFF7FFFu;
-      most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, m));
-    }
-  }
-  if (__any(most[0] >= 0x7F80 || most[1] >= 0x7F80)) {
-#pragma unroll 1
-    for (int i = 0; i < R * D / 512; ++i) {
-      typedef __attribute__((address_space(3))) u32x4 LdsWrite;
-      LdsWrite *at = (LdsWrite *)(tile + 1024 * i + 16 * lane);
-      u32x4 x = *at;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t lo = (x[k] & 0x7F80u) == 0x7F80u ? 0u : 0xFFFFu;
-        const uint32_t hi = (x[k] & 0x7F800000u) == 0x7F800000u ? 0u : 0xFFFF0000u;
-        x[k] &= lo | hi;
-      }
-      *at = x;
-    }
-    __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (3 << 14));  // lgkmcnt(0)
-    asm volatile("" ::: "memory");
-  }
-}
-
 // What is not finite in a tile, for a pass that has to tell what a query sees from what it does
 // not.  A fragment with zeros in such places:
 QL_DEV u32x4 finite(u32x4 x) {

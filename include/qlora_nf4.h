@@ -530,7 +530,9 @@ qlora_status_t qlora_rope(const uint16_t *Q, int64_t ldq, int32_t hq, const uint
  *
  * qlora_attn_bwd  the gradients of Q, K and V for the gradient dO of O, with O and lse as
  *  the forward gave them (of Q, K, V, spans, scale, cap and slopes as given to it).  Sums
- *  run in a fixed order.  dK and dV are summed over the query heads of their key head.
+ *  run in a fixed order.  dK and dV are summed over the query heads of their key head.  What
+ *  is not finite in a query, its dO or a key or value that it sees leaves the gradients that
+ *  the formulas make of it not finite, and no others.
  *  workspace: qlora_workspace_size(QLORA_OP_ATTN_BWD, M, hq, hk, d) bytes, 256-byte aligned.
  */
 qlora_status_t qlora_attn_spans(const int32_t *documents, int64_t n, const int32_t *prefix, int64_t M, int32_t causal,

@@ -111,6 +111,43 @@ def test_columns_of_a_value(M, hq, hk, d, cap, kind, value):
     spoiled(M, hq, hk, d, cap, kind, "V", value, ("O", "lse"))
 
 
+@pytest.mark.parametrize("what,value", [("Q", NAN), ("K", NAN), ("V", NAN), ("V", INF), ("dO", NAN), ("dO", INF)])
+@pytest.mark.parametrize("kind", ["causal", "documents"])
+@pytest.mark.parametrize("M,hq,hk,d,cap", SHAPES)
+def test_gradients(M, hq, hk, d, cap, kind, what, value):
+    spoiled(M, hq, hk, d, cap, kind, what, value, ("dQ", "dK", "dV"))
+
+
+@pytest.mark.parametrize("M,hq,hk,d,cap", [s for s in SHAPES if s[4] == 0.0])
+def test_scores_of_minus_infinity(M, hq, hk, d, cap):
+    p = problem(M, hq, hk, d, oracle.spans([0, M], M))
+    j, e = M // 2 + 1, 7
+    p["Q"][:, :, e] = -1.0
+    p["K"][j, :, e] = INF                                      # every score of key j: -inf
+    got = run(nf4, p)
+    seen = torch.arange(M, device=DEV) >= j
+    for k in ("O", "lse", "dV"):
+        assert bool(torch.isfinite(got[k]).all()), k
+    assert not got["dV"][j].any() and not got["dK"][j].any()
+    bad = torch.zeros_like(got["dQ"], dtype=torch.bool)
+    bad[seen, :, e] = True
+    assert torch.equal(~torch.isfinite(got["dQ"]), bad)
+    # the same without that key: spans cannot leave one key out, so the formulas in float64
+    q, k, v, do = (p[x].double() for x in ("Q", "K", "V", "dO"))
+    k, v = k.repeat_interleave(hq // hk, 1), v.repeat_interleave(hq // hk, 1)
+    row = M - 1
+    keep = torch.arange(M, device=DEV) != j
+    z = d ** -0.5 * torch.einsum("hd,jhd->hj", q[row], k[keep])
+    w = torch.softmax(z, 1)
+    O = torch.einsum("hj,jhd->hd", w, v[keep])
+    dP = torch.einsum("hd,jhd->hj", do[row], v[keep])
+    dS = w * (dP - (w * dP).sum(1, keepdim=True))
+    dQ = d ** -0.5 * torch.einsum("hj,jhd->hd", dS, k[keep])
+    at = torch.arange(d, device=DEV) != e
+    assert float((got["O"][row] - O).norm() / O.norm()) < 1e-2
+    assert float((got["dQ"][row][:, at] - dQ[:, at]).norm() / dQ[:, at].norm()) < 1e-2
+
+
 def test_one_new_token():
     """The same of one new token: a NaN of a query or a seen key reaches its whole row, of a
     value its value."""
