@@ -378,7 +378,8 @@ qlora_status_t qlora_attn_spans(const int32_t *documents, int64_t n, const int32
   if (!documents || !spans || n < 1 || M < 1 || window < 0) return QLORA_ERR_INVALID_VALUE;
   if (!aligned(documents, 4) || !aligned(prefix, 4) || !aligned(spans, 8)) return QLORA_ERR_INVALID_VALUE;
   if (!attn_supported(M, 1) || n > ((int64_t)1 << 31) - 2) return QLORA_ERR_UNSUPPORTED;
-  return launch_status(launch_attn_spans(documents, n, prefix, M, causal != 0, window, spans,
+  // (as wide as the tokens, a window leaves nothing out; wider ones could pass 64 bits)
+  return launch_status(launch_attn_spans(documents, n, prefix, M, causal != 0, window < M ? window : 0, spans,
                                          reinterpret_cast<hipStream_t>(stream)));
 }
 
