@@ -461,8 +461,7 @@ qlora_status_t qlora_decode_attn(const uint16_t *Q, const uint16_t *k_pages, con
   if (need && (!workspace || !aligned(workspace, 256) || ws_bytes < need)) return QLORA_ERR_INVALID_VALUE;
   const CacheShape c{const_cast<uint16_t *>(k_pages), const_cast<uint16_t *>(v_pages), pages, hk, page, d};
   const int seen = (int)(window < width * page ? window : 0);
-  const DecodeArgs a{c, Q, table, lens, slopes, scale, cap, seen, B, hq, width, O,
-                     reinterpret_cast<float *>(workspace)};
+  const DecodeArgs a{c, Q, table, lens, slopes, scale, cap, seen, B, hq, width, O, workspace};
   return launch_status(launch_decode_attn(a, reinterpret_cast<hipStream_t>(stream)));
 }
 

@@ -32,7 +32,7 @@ struct DecodeArgs {
   int hq;
   int64_t width;
   uint16_t *O;           // [B][hq][d]
-  float *part;           // the workspace (nullptr: none needed)
+  void *workspace;       // (nullptr: none needed)
 };
 
 size_t decode_workspace(int64_t B, int hq, int hk, int64_t capacity);
