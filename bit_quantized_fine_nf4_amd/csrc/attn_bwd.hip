@@ -25,10 +25,11 @@
 // for the weights' phase, as the forward has.
 //
 // D from the forward's bf16 O is off by a rounding of O, which all of a row's dS share: with
-// few keys, whose dS nearly cancel, that would be percents of dQ.  Workgroups whose queries
-// see at most 256 keys each, or whose head's bias leaves weight to a few tens (1531 tokens, heads
-// biased by 0.5 a token: dQ off by 0.0028 of its norm, so 0.0024), sum D = sum_j p_ij dP_ij
-// in a pass of its own instead.
+// few keys, whose dS nearly cancel, that would be percents of dQ.  Queries that see at most
+// 256 keys, or whose head's bias leaves weight to a few tens (1531 tokens, heads biased by 0.5 a
+// token: dQ off by 0.0028 of its norm, so 0.0024), have D = sum_j p_ij dP_ij in a pass of its own
+// over the keys of such queries instead.  Which one is a query's own matter: what else is in its
+// workgroup changes nothing.
 
 #include "attn_tiles.h"
 
@@ -97,7 +98,7 @@ inline BwdWork bwd_work(int64_t M, int64_t hq, int64_t hk, void *ws) {
 template <int D, Form FORM, int KG>
 __global__ __launch_bounds__(kThreads * KG, 2) void attn_dq_kernel(AttnArgs a, AttnGrads gr, BwdWork w) {
   __shared__ __attribute__((aligned(1024))) uint16_t ring[KG][4 * kTile * D];  // K, V; two slots
-  __shared__ int ends[3 * kWaves], spoiled[kWaves * KG];
+  __shared__ int ends[4 * kWaves], spoiled[kWaves * KG];
   __shared__ float owns[KG][kWaves][kWave];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kg = wave / kWaves, wv = wave % kWaves;
@@ -112,8 +113,14 @@ __global__ __launch_bounds__(kThreads * KG, 2) void attn_dq_kernel(AttnArgs a, A
   const Span span = span_of(a.spans, row, a.M);
   const Reach reach = reach_of(span);
   const bool any = span.lo < span.hi;
-  const int widest = rows_max(any ? span.hi - span.lo : 0);
-  if (kg == 0 && lane == 0) ends[wv] = reach.lo, ends[kWaves + wv] = reach.hi, ends[2 * kWaves + wv] = widest;
+  const float slope2 = FORM != kPlain && a.slopes ? a.slopes[head] * kLog2e : 0.0f;
+  // whether this query has D by its own sum, and the keys of the wave's that do
+  const bool sums = any && (span.hi - span.lo <= kFewKeys || (FORM != kPlain && slope2 >= kSteep * kLog2e));
+  const int own_lo = rows_min(sums ? span.lo : 0x7FFFFFFF), own_hi = rows_max(sums ? span.hi : 0);
+  if (kg == 0 && lane == 0) {
+    ends[wv] = reach.lo, ends[kWaves + wv] = reach.hi;
+    ends[2 * kWaves + wv] = own_lo, ends[3 * kWaves + wv] = own_hi;
+  }
   u32x4 qf[D / 16], df[D / 16];
   load_rows<D>(qf, a.Q + row * a.ldq + (int64_t)head * a.d, live, a.d, g);
   load_rows<D>(df, gr.dO + (row * a.hq + head) * a.d, live, a.d, g);
@@ -138,17 +145,19 @@ __global__ __launch_bounds__(kThreads * KG, 2) void attn_dq_kernel(AttnArgs a, A
       w.reach[row >> 5] = int4{reach.lo, reach.hi, gap ? 0x7FFFFFFF : reach.all_lo, reach.all_hi};
   }
   __syncthreads();
-  int first = ends[0], last = ends[kWaves];
-  const float slope2 = FORM != kPlain && a.slopes ? a.slopes[head] * kLog2e : 0.0f;
-  bool few = ends[2 * kWaves] <= kFewKeys;
+  // the workgroup's: least and most over the waves; nothing is seen: 0 to 0 (the least was INT_MAX)
+  auto from_to = [&](const int *lo, const int *hi, int &first, int &last) {
+    first = lo[0], last = hi[0];
 #pragma unroll
-  for (int v = 1; v < kWaves; ++v) {
-    first = ends[v] < first ? ends[v] : first;
-    last = ends[kWaves + v] > last ? ends[kWaves + v] : last;
-    few = few && ends[2 * kWaves + v] <= kFewKeys;
-  }
-  first = __builtin_amdgcn_readfirstlane(first < last ? first : last);  // (nothing is seen: first was INT_MAX)
-  last = __builtin_amdgcn_readfirstlane(last);
+    for (int v = 1; v < kWaves; ++v) {
+      first = lo[v] < first ? lo[v] : first;
+      last = hi[v] > last ? hi[v] : last;
+    }
+    first = __builtin_amdgcn_readfirstlane(first < last ? first : last);
+    last = __builtin_amdgcn_readfirstlane(last);
+  };
+  int first, last;
+  from_to(ends, ends + kWaves, first, last);
 
   f32x16 acc[D / 32];
   const float c = a.scale * kLog2e;
@@ -249,35 +258,37 @@ __global__ __launch_bounds__(kThreads * KG, 2) void attn_dq_kernel(AttnArgs a, A
           spoil<D>(acc, kt, r, k0 + r >= span.lo && k0 + r < span.hi, g);
         }
   };
-  auto walk = [&](auto pass) {
+  auto walk = [&](auto pass, int first, int last, int lo, int hi) {  // the workgroup's keys, the wave's
     int slot = 0;
     if (first + kg * kTile < last) fetch(first + kg * kTile, 0);
     for (int at = first; at < last; at += KG * kTile, slot ^= 1) {
       const int k0 = at + kg * kTile;
       tile_sync();
       if (k0 + KG * kTile < last) fetch(k0 + KG * kTile, slot ^ 1);
-      if (k0 >= reach.hi || k0 + kTile <= reach.lo) continue;
+      if (k0 >= hi || k0 + kTile <= lo) continue;
       step(k0, slot, k0 < reach.all_lo || k0 + kTile > reach.all_hi, pass);
     }
   };
-  if (few || (FORM != kPlain && slope2 >= kSteep * kLog2e)) {
-    walk(std::integral_constant<int, kOwnD>{});
+  int own_first, own_last;
+  from_to(ends + 2 * kWaves, ends + 3 * kWaves, own_first, own_last);
+  if (own_first < own_last) {
+    walk(std::integral_constant<int, kOwnD>{}, own_first, own_last, own_lo, own_hi);
     own = both_halves_sum(own);
     if constexpr (KG > 1) {
       owns[kg][wv][lane] = own;
       tile_sync();
       own = owns[0][wv][lane] + owns[1][wv][lane];
     }
-    if (any) delta = own;
+    if (sums) delta = own;
     tile_sync();  // the last tile is read
   }
   if (kg == 0 && g == 0) w.stat[head * w.ld + row] = f32x2{lse2, delta};
   zero(acc);
-  walk(std::integral_constant<int, kSums>{});
+  walk(std::integral_constant<int, kSums>{}, first, last, reach.lo, reach.hi);
   // (as in the forward: taken again if what masked keys hold has spoiled a sum)
   if (any_wave(any && !all_finite(acc), spoiled, wave, kWaves * KG)) {
     zero(acc);
-    walk(std::integral_constant<int, kCarefulSums>{});
+    walk(std::integral_constant<int, kCarefulSums>{}, first, last, reach.lo, reach.hi);
   }
   if constexpr (KG > 1) {
     static_assert(KG == 2, "one group's sums go to the other");
