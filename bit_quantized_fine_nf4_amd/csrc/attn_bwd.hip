@@ -43,7 +43,7 @@ constexpr int kRows = 32;     // queries per tile of attn_dkv
 // attn_dq's passes: D by its own sum; dQ; dQ where what is not finite is looked for
 enum { kOwnD, kSums, kCarefulSums };
 constexpr int kFewKeys = 256;
-constexpr float kSteep = 1.0f / 16;  // of a bias
+constexpr float kSteep = 1.0f / 16;  // of a bias, towards a query's own key or away from it
 
 struct BwdWork {
   f32x2 *stat;  // [hq][ld] lse in units of log2, and D
@@ -115,7 +115,7 @@ __global__ __launch_bounds__(kThreads * KG, 2) void attn_dq_kernel(AttnArgs a, A
   const bool any = span.lo < span.hi;
   const float slope2 = FORM != kPlain && a.slopes ? a.slopes[head] * kLog2e : 0.0f;
   // whether this query has D by its own sum, and the keys of the wave's that do
-  const bool sums = any && (span.hi - span.lo <= kFewKeys || (FORM != kPlain && slope2 >= kSteep * kLog2e));
+  const bool sums = any && (span.hi - span.lo <= kFewKeys || (FORM != kPlain && __builtin_fabsf(slope2) >= kSteep * kLog2e));
   const int own_lo = rows_min(sums ? span.lo : 0x7FFFFFFF), own_hi = rows_max(sums ? span.hi : 0);
   if (kg == 0 && lane == 0) {
     ends[wv] = reach.lo, ends[kWaves + wv] = reach.hi;

@@ -37,3 +37,12 @@ def test_few_keys_beside_many():
     spans[many] = torch.tensor([0, M])
     p = problem(M, hq, hk, d, spans.clamp(max=M))
     check(run(nf4, p), reference(p, d ** -0.5, own=(~many).to(DEV)))
+
+
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+def test_steep_negative_bias(cap):
+    """A bias that favours far keys leaves weight to a few of many keys as well: the oldest ones."""
+    M, hq, hk, d = 700, 4, 2, 64
+    p = problem(M, hq, hk, d, oracle.spans([0, M], M))
+    slopes = -torch.tensor([0.0625, 0.25, 0.5, 1.0], device=DEV)
+    check(run(nf4, p, cap=cap, slopes=slopes), reference(p, 0.125, cap, slopes, own=True))
