@@ -58,6 +58,12 @@ bool valid_heads(int32_t hq, int32_t hk, int32_t d, int32_t widest) {
 bool valid_scores(float scale, float cap, const float *slopes) {
   return scale > 0.0f && std::isfinite(scale) && cap >= 0.0f && std::isfinite(cap) && aligned(slopes, 4);
 }
+// The factors that the kernels form of them (in units of log2, their quotient) are then finite and
+// normal: an infinite one would make a score of zero NaN, and a cap past 2^127 is one.
+bool scores_supported(float scale, float cap) {
+  constexpr float kMost = 0x1p60f, kLeast = 0x1p-60f;
+  return scale >= kLeast && scale <= kMost && (cap == 0.0f || (cap >= kLeast && cap <= kMost));
+}
 // a launch has fewer than 2^32 threads: one workgroup of 256 for 128 queries of a head
 bool attn_supported(int64_t M, int32_t hq) {
   return M <= ((int64_t)1 << 24) && hq <= kMaxHeads && (M + 127) / 128 * hq < ((int64_t)1 << 24);
@@ -392,7 +398,9 @@ qlora_status_t qlora_attn_fwd(const uint16_t *Q, int64_t ldq, const uint16_t *K,
     return QLORA_ERR_INVALID_VALUE;
   if (!spans || !aligned(spans, 8) || !O || !lse || !aligned16({O, lse})) return QLORA_ERR_INVALID_VALUE;
   if (O == Q || O == K || O == V) return QLORA_ERR_INVALID_VALUE;
-  if (!attn_supported(M, hq) || ldq > kMaxStride || ldk > kMaxStride || ldv > kMaxStride) return QLORA_ERR_UNSUPPORTED;
+  if (!attn_supported(M, hq) || !scores_supported(scale, cap) || ldq > kMaxStride || ldk > kMaxStride ||
+      ldv > kMaxStride)
+    return QLORA_ERR_UNSUPPORTED;
   const AttnArgs a{Q, K, V, ldq, ldk, ldv, spans, slopes, scale, cap, M, hq, hk, d};
   return launch_status(launch_attn_fwd(a, O, lse, reinterpret_cast<hipStream_t>(stream)));
 }
@@ -415,7 +423,9 @@ qlora_status_t qlora_attn_bwd(const uint16_t *dO, const uint16_t *Q, int64_t ldq
       if (out[i] == p) return QLORA_ERR_INVALID_VALUE;
     if (out[i] == out[(i + 1) % 3]) return QLORA_ERR_INVALID_VALUE;
   }
-  if (!attn_supported(M, hq) || ldq > kMaxStride || ldk > kMaxStride || ldv > kMaxStride) return QLORA_ERR_UNSUPPORTED;
+  if (!attn_supported(M, hq) || !scores_supported(scale, cap) || ldq > kMaxStride || ldk > kMaxStride ||
+      ldv > kMaxStride)
+    return QLORA_ERR_UNSUPPORTED;
   if (!workspace || !aligned(workspace, 256) || ws_bytes < round256(attn_bwd_workspace(M, hq, hk, d)))
     return QLORA_ERR_INVALID_VALUE;
   const AttnArgs a{Q, K, V, ldq, ldk, ldv, spans, slopes, scale, cap, M, hq, hk, d};
@@ -455,7 +465,7 @@ qlora_status_t qlora_decode_attn(const uint16_t *Q, const uint16_t *k_pages, con
   if (!Q || !table || !lens || !O || !aligned16({Q, O}) || !aligned(table, 4) || !aligned(lens, 4) || O == Q)
     return QLORA_ERR_INVALID_VALUE;
   if (!cache_supported(pages, hk, page) || width > ((int64_t)1 << 30) / page ||
-      !decode_supported(B, hq, width * page))
+      !decode_supported(B, hq, width * page) || !scores_supported(scale, cap))
     return QLORA_ERR_UNSUPPORTED;
   const size_t need = round256(decode_workspace(B, hq, hk, width * page));
   if (need && (!workspace || !aligned(workspace, 256) || ws_bytes < need)) return QLORA_ERR_INVALID_VALUE;

@@ -515,7 +515,8 @@ qlora_status_t qlora_rope(const uint16_t *Q, int64_t ldq, int32_t hq, const uint
  * Query head h reads key head h / (hq / hk).
  *  Q [M][hq][d], K and V [M][hk][d] bf16 with token strides ldq, ldk, ldv; O, dO and the
  *  gradients are dense.  lse [hq][M] float32.  spans M x 2 int32, slopes hq float32 or NULL.
- *  scale > 0.  d a multiple of 8 up to 128, strides multiples of 8, hq a multiple of hk;
+ *  scale > 0, cap 0 (none) or more; either (but a cap of 0) outside 2^-60..2^60 is
+ *  QLORA_ERR_UNSUPPORTED.  d a multiple of 8 up to 128, strides multiples of 8, hq a multiple of hk;
  *  bf16 tensors and lse 16-byte aligned, spans 8, slopes 4.  Products are of bf16 operands
  *  with float32 sums: the softmax weights and score gradients are rounded to bf16 for the
  *  products that follow.  M > 2^24, hq > 4096, 2^24 or more stretches of 128 queries in all
