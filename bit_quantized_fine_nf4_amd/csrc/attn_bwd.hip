@@ -583,7 +583,12 @@ __global__ __launch_bounds__(kThreads * KG, 2) void attn_dkv_kernel(AttnArgs a, 
   };
   walk(std::false_type{});
   // (as in the forward: taken again if what masked queries hold has spoiled a sum)
-  if (any_wave(!(all_finite(dk) && all_finite(dv)), lds.spoiled, wave, kWaves * KG)) walk(std::true_type{});
+  if (any_wave(!(all_finite(dk) && all_finite(dv)), lds.spoiled, wave, kWaves * KG)) {
+    // (the keys again: kept for this pass, a register of the first one's products was spilled, whose
+    // return waits for the copies: 4001 tokens in 9 documents 154 us, so 150)
+    load_rows<D>(kf, a.K + (int64_t)key * a.ldk + (int64_t)hk * a.d, live, a.d, g);
+    walk(std::true_type{});
+  }
   __syncthreads();  // the last tiles are read
   __builtin_amdgcn_s_waitcnt(0);  // no copy may land after the workgroup's end
   if constexpr (KG > 1) {
