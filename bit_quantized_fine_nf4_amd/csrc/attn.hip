@@ -15,11 +15,16 @@
 //
 // Bound by the matrix cores and the weights' vector operations, which share a SIMD: two
 // waves on each take turns, one in its products while the other is in its softmax.
-// Measured, causal, heads of 128: 8192 tokens of 64 heads for 8 1.0 ms, 1.09 PFLOP/s; 2048
-// tokens of 64 heads 80 us, 0.86 PFLOP/s (at the former's rate 63: two rounds of workgroups,
-// each with a start and an end).  Matrix cores busy 38 % of the cycles there, no bank
-// conflicts.  Slower: six waves a workgroup; the next tile's products between this one's
-// weights (1.35 ms).
+//
+// The kernels of 64 values hold 124 to 126 registers, of 128 values 177 to 178 (capped 202 and 254).
+// Measured, causal, heads of 128: 8192 tokens of 64 heads for 8 1.04 ms, 1.06 PFLOP/s, matrix
+// cores busy 57 % of the cycles (1.14 in twelve traced passes, whose clock falls); 2048 tokens of
+// 64 heads 80 to 92 us, 0.86 PFLOP/s (at the former's rate 65: two rounds of workgroups, each
+// with a start and an end), busy 39 %; no bank conflicts.  Slower: six waves a workgroup; the
+// next tile's products between this one's weights (1.35 ms).
+//
+// Heads of 72 to 120 values take all products of 128, those of 8 to 56 those of 64: 2048 tokens
+// of 64 heads of 64, 80, 96, 112 and 128 values 61, 72, 74, 81 and 80 us.
 
 #include "attn_tiles.h"
 
@@ -297,7 +302,8 @@ static hipError_t launch_fwd(const AttnArgs &a, uint16_t *O, float *lse, hipStre
 }
 
 // Two groups of waves where one would leave compute units, which hold two workgroups of four
-// waves, half empty or with one long workgroup each.  One and two groups, 128 values a head, causal:
+// waves, half empty or with one long workgroup each.  Heads of 64 values and fewer take the same
+// rule, whose sides were measured at 128.  One and two groups, 128 values a head, causal:
 //   256 workgroups   256 tokens 12.2, 12.2 us    1000  25.6, 22.0    4096   77, 59    8192  146, 112
 //   512              1000 tokens 30.7, 32.7      2048  51.8, 46.7    8192  178, 140
 //   768 and more     2048 tokens 60, 72          4096 (1024 workgroups)  138, 152

@@ -18,11 +18,14 @@
 // p and dS are rounded to bf16 as operands of the products that follow.
 //
 // Bound by the matrix cores, the weights' vector operations beside them and the waits between
-// dependent products: at 256 registers a wave two fit a SIMD.  Measured, causal, heads of
-// 128: 2048 tokens of 64 heads dQ 119 us, dK and dV 149 to 158 (0.94 PFLOP/s by the seven
-// products, matrix cores busy 42 and 41 % of the cycles, no bank conflicts); 4001 tokens in 9
-// documents, 32 heads for 8, dQ 87, dK and dV 141 and their sum 12.  No gain: raised priority
-// for the weights' phase, as the forward has.
+// dependent products: two waves fit a SIMD at the 224 to 251 registers that dQ takes at 128
+// values and the 253 to 256 of dK and dV (up to 10 more are spilled, none within the plain form's
+// products); at 64 values 148 to 188 let a unit hold one workgroup of eight waves or, except
+// capped ones, three of four.  Measured, causal, heads of 128: 2048 tokens of 64 heads dQ 119
+// to 148 us, dK and dV 149 to 195 (the clock falls; 0.94 PFLOP/s by the seven products, matrix
+// cores busy 42 % of the cycles, no bank conflicts); 4001 tokens in 9 documents, 32 heads for 8,
+// dQ 94, dK and dV 150 and their sum 12.  No gain: raised priority for the weights' phase, as
+// the forward has.
 //
 // D from the forward's bf16 O is off by a rounding of O, which all of a row's dS share: with
 // few keys, whose dS nearly cancel, that would be percents of dQ.  Queries that see at most
@@ -63,7 +66,7 @@ inline int64_t padded(int64_t M) { return (M + 127) / 128 * 128; }
 // tiles alone 142 us, so 32).  Their sums go through the workspace in the time of six tiles.
 // So a part keeps 4 tiles up to two parts for each unit, 16 up to four, and 128 beyond,
 // where long documents' workgroups need not wait for longer ones.  Backward in us, in 1, 2, 4,
-// 8, 16 and 32 parts by tiles:
+// 8, 16 and 32 parts by tiles, 128 values a head (64 take the same rule):
 //   tokens  heads  key heads   of 128 keys
 //     512     32       8          32       111,   80,   63,  52,  51,  71
 //    2048      8       1          16       682,  462,  264, 165, 118,  97
@@ -638,7 +641,7 @@ static hipError_t launch_both(const AttnArgs &a, const AttnGrads &g, const BwdWo
   const dim3 gk((uint32_t)((a.M + kKeysWg - 1) / kKeysWg * a.hk * w.splits));
   // Two groups of waves where one leaves compute units half empty; a second round of workgroups
   // (there is room for one of each kind a unit) is short if there are many tokens.  Backward with
-  // one and two, 128 values a head, causal:
+  // one and two, 128 values a head (64 take the same rule), causal:
   //   256 workgroups   256 tokens 44, 44 us   1000   83, 81    2048  127, 121   4096  215, 201
   //   288 to 384       1000 tokens 110, 118   1500  106, 101   2000  148, 148   4096  245, 228
   //   512              1000 tokens 97, 105    2048  170, 170   8192  564, 532

@@ -226,7 +226,7 @@ QL_DEV float both_halves_sum(float x) {
 // Chebyshev's points, which leaves 2^-26.  Scores of a cap in use hardly ever pass half of it, so
 // a wave looks its values over first and takes the exponentials only if one does: step of 1531
 // tokens, 24 heads of 64, cap 30 109 us, by exponentials alone 123, by both everywhere 141; of 2048
-// tokens, 32 heads of 128, cap 30 253 (251), cap 4, which most tiles pass half of, 302 (251).
+// tokens, 32 heads of 128, cap 30 253 (251), cap 4, which most tiles pass half of, 292 (257).
 constexpr float kTanhSmall = 1.4426950408889634f;  // |x| at |t| = 1/2
 template <bool FAR>
 QL_DEV float tanh_of(float x) {
@@ -305,7 +305,8 @@ QL_DEV Reach reach_of(const Span &s) {
 
 // Workgroup -> (tile, head): with a multiple of eight heads each XCD (workgroups go to the
 // eight in turn, each with its own L2) takes whole heads, so that the tiles of a head find
-// its keys and values in L2.  Tiles are the slow index, so that the longest of all heads
+// its keys and values in L2 (so the steep heads of a geometric bias, whose dQ takes a pass more, are
+// together on half of the XCDs).  Tiles are the slow index, so that the longest of all heads
 // start first (2048 causal tokens, 64 heads, forward: 79 us; head after head 104).
 QL_DEV void unit_place(int unit, int tiles, int heads, int &tile, int &head) {
   if ((heads & 7) == 0) {

@@ -4,7 +4,8 @@
 //   z_j = scale q . k_j,  capped: cap tanh(z / cap),  biased: z - slope (n - 1 - j)
 //   O   = sum_j softmax(z)_j v_j   over max(0, n - window) <= j < n.
 // Bound by reading the keys and values once.  Measured: 48 sequences of up to 8192 tokens, 64
-// heads for 8 (152 MB) 32 us and 5 for the join, 4.7 TB/s of the first; such of 805 MB in all
+// heads for 8 (152 MB) 32 us and 4 for the join, 4.7 TB/s of the first (with a cap or a bias the
+// same within a microsecond, with a window of 1000 tokens 21 us in all); such of 805 MB in all
 // 164 us, 4.9 TB/s; one of 2049 tokens, 32 heads (34 MB) 9 and 4 us, too short to fill the
 // memory with copies.
 //
@@ -22,7 +23,9 @@
 // wave always has copies in flight.  The heads are the 16 columns of
 // v_mfma_f32_16x16x32_bf16: with one head fifteen of them are idle, and the matrix cores still
 // take a tenth of the time that the copies take.  The waves' results are joined through
-// LDS; those of several stretches through the workspace, in a second kernel.
+// LDS; those of several stretches through the workspace, in a second kernel.  More than 16 heads
+// for a key head are several items, which read its keys and values again, from the last-level
+// cache at best: that batch with one key head for 64 heads (20 MB) 30 us, for 16 21.
 //
 // A copy's rows are of one page (pages have 8 tokens or more): its descriptor begins at the
 // row in the page and ends where the sequence does, so rows past the end, like those of a

@@ -504,7 +504,7 @@ qlora_status_t qlora_rope(const uint16_t *Q, int64_t ldq, int32_t hq, const uint
 /*
  * Attention of packed tokens, each query over one span of keys.  With spans[i] = (lo, hi),
  * query i sees the keys lo <= j < hi (clamped to [0, M); none if lo >= hi):
- *   z_ij = scale * q_i . k_j        cap > 0:  z <- cap * tanh(z / cap)
+ *   z_ij = scale * q_i . k_j        cap > 0:  z <- cap * tanh(z / cap), off by roundings of z
  *                                   slopes:   z <- z - slopes[head] * |i - j|
  *   O_i  = sum_j softmax(z_i)_j v_j,   lse_i = log sum_j exp(z_ij)
  * A query that sees nothing has O = 0, lse = -inf, passes no gradient, and its rows of Q,
@@ -534,6 +534,8 @@ qlora_status_t qlora_rope(const uint16_t *Q, int64_t ldq, int32_t hq, const uint
  *  run in a fixed order.  dK and dV are summed over the query heads of their key head.  What
  *  is not finite in a query, its dO or a key or value that it sees leaves the gradients that
  *  the formulas make of it not finite, and no others.
+ *  A query's D = sum_j softmax(z)_j (dO . v_j) is dO . O with the bf16 O, or, if it sees at most
+ *  256 keys or its head's |slope| is 1/16 or more, that sum: by its own span and head alone.
  *  workspace: qlora_workspace_size(QLORA_OP_ATTN_BWD, M, hq, hk, d) bytes, 256-byte aligned.
  */
 qlora_status_t qlora_attn_spans(const int32_t *documents, int64_t n, const int32_t *prefix, int64_t M, int32_t causal,
@@ -568,7 +570,7 @@ qlora_status_t qlora_attn_bwd(const uint16_t *dO, const uint16_t *Q, int64_t ldq
  *   Q, O    [B][hq][d], dense.   table  [B][width] int32: the page of tokens page * e ..
  *   lens    B int32, clamped to 0..width * page; 0 gives O = 0.
  *  Tokens whose page is not in the cache count as masked.  Pages and tokens that a sequence
- *  does not see are not read.
+ *  does not see are not read.  NaN and infinities that it sees reach O as in qlora_attn_fwd.
  *  workspace: qlora_workspace_size(QLORA_OP_DECODE_ATTN, B, hq, width * page, hk) bytes,
  *  256-byte aligned (0: not needed).
  *  More than 2^30 slots or 2^30 tokens of capacity (width * page), M > 2^31, n > 2^23,
