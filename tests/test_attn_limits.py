@@ -12,7 +12,7 @@ A = [ctypes.c_void_p(0x100000 + 0x10000 * i) for i in range(16)]   # distinct, a
 
 
 def call(name, scale, cap, M=0):
-    """With M = 0 the sizes are refused after nothing: QLORA_ERR_INVALID_VALUE for any scale."""
+    """M = 0 is invalid whatever the scale: sizes are looked at before limits."""
     if name == "fwd":
         return lib.qlora_attn_fwd(A[0], 128, A[1], 128, A[2], 128, A[3], None, scale, cap, M, 1, 1, 128, A[4], A[5], None)
     if name == "bwd":
